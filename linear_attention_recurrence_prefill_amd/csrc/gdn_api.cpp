@@ -13,6 +13,7 @@
 
 #include "../../include/gdn.h"
 #include "../../include/gdn_calib.h"
+#include "gdn_api_util.h"
 #include "gdn_bwd_internal.h"
 #include "gdn_calib_internal.h"
 #include "gdn_decode.h"
@@ -21,9 +22,11 @@
 static_assert(GDN_NOALLOC_SCRATCH_BYTES == gdn::kStaticScratchBytes,
               "the header's scratch size is the library's");
 
+namespace gdn {
+namespace api {
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
 
 gdn_status fail(gdn_status s, const char *fmt, ...) {
   va_list ap;
@@ -41,7 +44,9 @@ gdn_status hip_fail(hipError_t e, const char *what) {
 // validates cu_seqlens on the device and returns GDN_ERR_BAD_SHAPE before any compute launch if
 // it is malformed or differs from the host copy the call was given, and after its launches
 // synchronises the stream and returns GDN_ERR_DEVICE_CHECK if a kernel set a fault flag.
+namespace {
 std::atomic<int> g_debug{-1};
+}  // namespace
 
 bool debug_on() {
   int d = g_debug.load(std::memory_order_relaxed);
@@ -111,6 +116,7 @@ uint32_t *fault_word() {
   return gdn::device_check_words(&words) == hipSuccess ? words + 1 : nullptr;
 }
 
+namespace {
 // Per-device properties cache: is the device gfx950, and its CU count.
 struct DevInfo {
   int checked = 0;
@@ -121,7 +127,37 @@ constexpr int kMaxDevices = 64;
 DevInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
-gdn_status device_info(int *cus);
+}  // namespace
+
+gdn_status device_info(int *cus) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(GDN_ERR_UNSUPPORTED_ARCH, "device %d", dev);
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  DevInfo &d = g_dev[dev];
+  if (!d.checked) {
+    hipDeviceProp_t prop;
+    e = hipGetDeviceProperties(&prop, dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
+    d.is_gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    d.cus = prop.multiProcessorCount;
+    d.checked = 1;
+  }
+  if (!d.is_gfx950) return fail(GDN_ERR_UNSUPPORTED_ARCH, "device %d is not gfx950", dev);
+  if (cus) *cus = d.cus;
+  return GDN_OK;
+}
+
+const char *last_error() { return g_err; }
+void set_debug_on(bool on) { g_debug.store(on ? 1 : 0, std::memory_order_relaxed); }
+
+}  // namespace api
+}  // namespace gdn
+
+using namespace gdn::api;
+
+namespace {
 
 // The forward kernel a problem runs on: for bf16 inputs the warp-specialised pipeline (d = 128)
 // or the 8-wave kernel (d = 64); otherwise the general kernel (fp32 inputs, and the variant that
@@ -151,28 +187,6 @@ gdn_status parallel_slots(const gdn_problem *p, bool dump, int *slots) {
   return GDN_OK;
 }
 
-gdn_status device_info(int *cus) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-  if (dev < 0 || dev >= kMaxDevices) return fail(GDN_ERR_UNSUPPORTED_ARCH, "device %d", dev);
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  DevInfo &d = g_dev[dev];
-  if (!d.checked) {
-    hipDeviceProp_t prop;
-    e = hipGetDeviceProperties(&prop, dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
-    d.is_gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    d.cus = prop.multiProcessorCount;
-    d.checked = 1;
-  }
-  if (!d.is_gfx950) return fail(GDN_ERR_UNSUPPORTED_ARCH, "device %d is not gfx950", dev);
-  if (cus) *cus = d.cus;
-  return GDN_OK;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 gdn_status check_problem(const gdn_problem *p) {
   if (!p) return fail(GDN_ERR_NULL_ARG, "problem is NULL");
   if (p->total_tokens < 0 || p->total_tokens > INT32_MAX)
@@ -201,8 +215,6 @@ gdn_status check_problem(const gdn_problem *p) {
   if (!std::isfinite(p->scale)) return fail(GDN_ERR_BAD_SHAPE, "scale must be finite");
   return GDN_OK;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Heads of q and k (num_k_heads, 0 meaning one per value head).
 int32_t k_heads(const gdn_problem *p) { return p->num_k_heads > 0 ? p->num_k_heads : p->num_heads; }
@@ -280,9 +292,6 @@ gdn_status check_cu_host(const gdn_problem *p, const int32_t *cu_host) {
     if (cu_host[n + 1] < cu_host[n]) return fail(GDN_ERR_BAD_SHAPE, "cu_seqlens_host descends");
   return GDN_OK;
 }
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // The exact mode's split (three passes: every unit's affine map (B, M) from its chunks, the maps
 // composed along each sequence into true start states, every unit rerun from its start) is built
@@ -1024,7 +1033,7 @@ gdn_status gdn_validate_cu_seqlens(const int32_t *cu_seqlens, int32_t num_seqs,
 
 gdn_status gdn_set_debug(int32_t on) {
   if (on != 0 && on != 1) return fail(GDN_ERR_BAD_MODE, "on must be 0 or 1");
-  g_debug.store(on, std::memory_order_relaxed);
+  set_debug_on(on != 0);
   return GDN_OK;
 }
 
@@ -1063,6 +1072,6 @@ const char *gdn_status_string(gdn_status s) {
   return "unknown status";
 }
 
-const char *gdn_last_error(void) { return g_err; }
+const char *gdn_last_error(void) { return last_error(); }
 
 }  // extern "C"

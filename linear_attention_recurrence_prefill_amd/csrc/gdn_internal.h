@@ -21,6 +21,9 @@ constexpr uint32_t kCuLastNotTotal = 4u;  // cu[N] != T
 constexpr uint32_t kCuOutOfRange = 8u;    // some cu[n + 1] outside [0, T]
 // Fault flags kernels set in the per-device check words (gdn_device_faults).
 constexpr uint32_t kFaultDiagWait = 1u;   // a bounded wait between the forward's waves ran out
+constexpr uint32_t kFaultPageRange = 2u;  // a page outside its pool, or a parent that is not live
+constexpr uint32_t kFaultPageTwice = 4u;  // a page written twice, or read and written, by one call
+constexpr uint32_t kFaultNoPage = 8u;     // a fork found no free page
 
 // Bytes of the static device scratch array behind gdn_chunk_fwd_noalloc (gdn_noalloc.hip).
 constexpr size_t kStaticScratchBytes = (size_t)128 << 20;

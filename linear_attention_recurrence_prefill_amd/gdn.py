@@ -20,13 +20,16 @@ GDN_DTYPE_F32, GDN_DTYPE_BF16 = 0, 1
 GDN_MODE_EXACT, GDN_MODE_TRUNCATE = 0, 1
 _MODES = {"exact": GDN_MODE_EXACT, "truncate": GDN_MODE_TRUNCATE}
 
-# Every exported entry point of include/gdn.h.
+# Every exported entry point of include/*.h.
 EXPORTS = ("gdn_problem_init", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd",
            "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_plan", "gdn_chunk_fwd_intermediates",
            "gdn_chunk_bwd_workspace_size",
            "gdn_chunk_bwd", "gdn_decode_step", "gdn_validate_cu_seqlens", "gdn_set_debug",
            "gdn_get_debug", "gdn_device_faults", "gdn_status_string", "gdn_last_error",
-           "gdn_calib_copy", "gdn_calib_mfma_bf16")
+           "gdn_calib_copy", "gdn_calib_mfma_bf16",
+           "gdn_linattn_fwd_workspace_size", "gdn_linattn_bwd_workspace_size", "gdn_linattn_fwd",
+           "gdn_linattn_bwd", "gdn_linattn_step", "gdn_pages_workspace_size", "gdn_pages_copy",
+           "gdn_pages_fork", "gdn_pages_free", "gdn_pages_compact")
 
 # Status bits of gdn_validate_cu_seqlens.
 CU_FIRST_NOT_ZERO, CU_DESCENDING, CU_LAST_NOT_TOTAL, CU_OUT_OF_RANGE = 1, 2, 4, 8
@@ -104,6 +107,10 @@ def load_library() -> ctypes.CDLL:
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
     lib.gdn_last_error.restype = ctypes.c_char_p
+    from . import linattn, pages
+
+    linattn._declare(lib)
+    pages._declare(lib)
     _lib = lib
     return lib
 
