@@ -47,6 +47,8 @@ struct LinArgs {
   float scale;
 };
 
+// Workgroups of the passes that one CU holds at once (registers and LDS).
+inline int linattn_blocks_per_cu(int D, bool bf16) { return bf16 || D == 64 ? 2 : 1; }
 hipError_t launch_linattn_pass(const LinArgs &a, int D, bool bf16, LinPass pass, hipStream_t stream);
 // The states at the units' starts (rev: the state gradients at their ends) from the units' sums.
 hipError_t launch_linattn_scan(const LinArgs &a, int D, bool rev, hipStream_t stream);

@@ -78,12 +78,18 @@ __device__ __forceinline__ F2 log2_decay(float g) {
 // the product itself, for both input types.
 template <class E>
 struct Op;
+// bf16 tiles: rows of D + 16 elements (8 (mod 64) banks apart), and in every other group of eight
+// rows the 16-byte units are exchanged in pairs.  The eight rows that a half wave's transposing
+// read takes then lie on different banks, and so do the sixteen rows of a row read.
 template <>
 struct Op<bf16> {
   typedef bf16x8 Frag;
-  static constexpr int kPad = 8;
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  static constexpr int kPad = 16;
+  // where column `col` of row `row` is within the row (col in units that stay whole: 4 elements)
+  static __device__ __forceinline__ int place(int row, int col) { return col ^ (row & 8); }
   static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return mma_bf16(a, b, c); }
-  // a row: p at the row's first index plus 4 gq
+  // a row, from its element at index 4 gq on (a multiple of 32 further: the next products')
   static __device__ __forceinline__ Frag row(const bf16 *p) {
     return cat8(lds_bf16x4(p), lds_bf16x4(p + 16));
   }
@@ -91,10 +97,32 @@ struct Op<bf16> {
   template <int LD>
   static __device__ __forceinline__ Frag column(const bf16 *tile, int row0, int colq, int, int c,
                                                 int gq) {
-    const bf16 *p = tile + (row0 + 4 * gq + (c >> 2)) * LD + colq;
+    const int r = 4 * gq + (c >> 2);
+    const bf16 *p = tile + (row0 + r) * LD + place(r, colq);
     return cat8(lds_tr16(p), lds_tr16(p + 16 * LD));
   }
   static __device__ __forceinline__ Frag round(f32x4 a, f32x4 b) { return to_bf16x8(a, b); }
+  // a, b less what round() made of them: x - hi is one dot product with (-1, 0) or (0, -1).  The
+  // pairs are kept in registers: as an inline constant the compiler writes (-1, 0) as the fp32
+  // -1.0, which is the other pair.
+  static __device__ __forceinline__ void residual(Frag f, f32x4 &a, f32x4 &b) {
+    unsigned u0 = 0x0000bf80u, u1 = 0xbf800000u;
+    asm("" : "+s"(u0), "+s"(u1));
+    const bf16x2 e0 = __builtin_bit_cast(bf16x2, u0), e1 = __builtin_bit_cast(bf16x2, u1);
+    const bf16x2 f0 = {f[0], f[1]}, f1 = {f[2], f[3]}, f2 = {f[4], f[5]}, f3 = {f[6], f[7]};
+    a = f32x4{__builtin_amdgcn_fdot2_f32_bf16(f0, e0, a[0], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f0, e1, a[1], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f1, e0, a[2], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f1, e1, a[3], false)};
+    b = f32x4{__builtin_amdgcn_fdot2_f32_bf16(f2, e0, b[0], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f2, e1, b[1], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f3, e0, b[2], false),
+              __builtin_amdgcn_fdot2_f32_bf16(f3, e1, b[3], false)};
+  }
+  // two stored tiles side by side
+  static __device__ __forceinline__ Frag pair(const bf16 *p, int next) {
+    return cat8(lds_bf16x4(p), lds_bf16x4(p + next));
+  }
   static __device__ __forceinline__ f32x4 lo_part(Frag f) {
     return f32x4{(float)f[0], (float)f[1], (float)f[2], (float)f[3]};
   }
@@ -109,6 +137,7 @@ template <>
 struct Op<float> {
   typedef F32x8 Frag;
   static constexpr int kPad = 4;
+  static __device__ __forceinline__ int place(int, int col) { return col; }
   static __device__ __forceinline__ f32x4 mma(Frag x, Frag y, f32x4 c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) c = mma_f32(x.a[j], y.a[j], c);
@@ -132,25 +161,13 @@ struct Op<float> {
     return f;
   }
   static __device__ __forceinline__ Frag round(f32x4 a, f32x4 b) { return F32x8{a, b}; }
+  static __device__ __forceinline__ void residual(Frag, f32x4 &, f32x4 &) {}
+  static __device__ __forceinline__ Frag pair(const float *p, int next) {
+    return F32x8{lds_f32x4(p), lds_f32x4(p + next)};
+  }
   static __device__ __forceinline__ f32x4 lo_part(Frag f) { return f.a; }
   static __device__ __forceinline__ f32x4 hi_part(Frag f) { return f.b; }
 };
-
-// c + (a as a sum of TERMS rounded operands) . b, or with b the split one.
-template <class E, int TERMS, bool SPLIT_A>
-__device__ __forceinline__ f32x4 mma_split(f32x4 s0, f32x4 s1, typename Op<E>::Frag o, f32x4 c) {
-  typedef Op<E> X;
-#pragma unroll
-  for (int i = 0; i < TERMS; ++i) {
-    const typename X::Frag f = X::round(s0, s1);
-    c = SPLIT_A ? X::mma(f, o, c) : X::mma(o, f, c);
-    if (i + 1 < TERMS) {
-      s0 -= X::lo_part(f);
-      s1 -= X::hi_part(f);
-    }
-  }
-  return c;
-}
 
 template <class E>
 __device__ __forceinline__ void store4(E *p, f32x4 x);
@@ -186,15 +203,34 @@ struct PassTraits {
   static constexpr int kTiles = kSum ? 2 : (kDots ? 4 : 3);
 };
 
+// The 64 x 64 products P in LDS, by 16 x 16 tiles (16 rows of x, 16 of y) in operand order: the
+// tiles that a row of tiles needs (two at a time; a masked partner is stored as zeros).
+template <bool REV>
+__device__ __forceinline__ int p_slot(int xt, int yt) {
+  if (REV) return (xt == 0 ? 0 : xt == 1 ? 4 : xt == 2 ? 8 : 10) + yt - (xt & 2);
+  return (xt == 0 ? 0 : xt == 1 ? 2 : xt == 2 ? 4 : 8) + yt;
+}
+constexpr int kPSlots = 12;
+template <class E>
+constexpr int p_terms() {
+  return sizeof(E) == 2 ? 2 : 1;
+}
+template <class E>
+constexpr size_t p_bytes() {
+  return (size_t)kPSlots * 64 * 4 * sizeof(E) * p_terms<E>();
+}
+
 template <class E, int D, int PASS>
-constexpr size_t pass_tile_bytes() {
-  return (size_t)PassTraits<PASS>::kTiles * 64 * (D + Op<E>::kPad) * sizeof(E);
+constexpr size_t pass_lds_bytes() {
+  typedef PassTraits<PASS> PT;
+  const size_t tile = (size_t)64 * (D + Op<E>::kPad) * sizeof(E);
+  return PT::kTiles * tile + (PT::kSum || PT::kDots ? 0 : p_bytes<E>());
 }
 
 }  // namespace
 
 template <class E, int D, int PASS>
-__global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(LinArgs a) {
   typedef Op<E> X;
   typedef typename X::Frag Frag;
   typedef PassTraits<PASS> PT;
@@ -208,19 +244,23 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
   // terms of the split operands (see the file's head)
   constexpr bool kB = sizeof(E) == 2;
   constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);
-  constexpr int kPTerms = kB ? 2 : 1;
+  constexpr int kPTerms = p_terms<E>();
+  constexpr int kDecayWave = PT::kRev ? 3 : 0;  // the wave with the fewest tiles of P
 
   extern __shared__ __attribute__((aligned(16))) char smem[];
   E *const ty = reinterpret_cast<E *>(smem);   // tiles [64][LD]: y, z, x, w
   E *const tz = ty + 64 * LD;
   E *const tx = tz + 64 * LD;
   E *const tw = tx + 64 * LD;
-  __shared__ __attribute__((aligned(16))) float g_hi[64], g_lo[64], f_x[64], f_y[64];
+  // P: behind the tiles, or (four tiles) over x, which is dead by then
+  E *const tp = PT::kDots ? tx : tx + 64 * LD;
+  __shared__ __attribute__((aligned(16))) float g_hi[64], g_lo[64], f_x[64], f_y[64], f_a[64], f_b[64];
   __shared__ float sh_decay;
-  __shared__ float dots[4][64], rsum[64], csum[4][64];
+  __shared__ float dots[2][4][64], rsum[2][64], csum[2][4][64];  // by the chunk's parity
   __shared__ int sh_unit[4];
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, gq = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, gq = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.y, hk = h / (a.H / a.HK);
 
   if (w == 0) {
@@ -233,7 +273,9 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
     }
   }
   __syncthreads();
-  const int seq = sh_unit[0], c0 = sh_unit[1], c1 = sh_unit[2];
+  const int seq = __builtin_amdgcn_readfirstlane(sh_unit[0]);
+  const int c0 = __builtin_amdgcn_readfirstlane(sh_unit[1]);
+  const int c1 = __builtin_amdgcn_readfirstlane(sh_unit[2]);
   if (seq < 0) return;
   const int64_t t_beg = a.cu[seq], t_end = a.cu[seq + 1];
   if (t_beg < 0 || t_end < t_beg || t_end > a.T) return;
@@ -248,8 +290,8 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
   }
 
   // the rows of this pass
-  const void *px, *py, *pz, *pw = nullptr;
-  int hx = h, hy = h, hz = h, hw = hk, nx = a.H, ny = a.H, nz = a.H;
+  const void *px = nullptr, *py, *pz, *pw = nullptr;
+  int hx = h, hy = h, hz = h, nx = a.H, ny = a.H, nz = a.H;
   if (PASS == kLinFwd) {
     px = a.q, py = a.k, pz = a.v, hx = hy = hk, nx = ny = a.HK;
   } else if (PASS == kLinDq) {
@@ -259,9 +301,9 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
   } else if (PASS == kLinDk) {
     px = a.v, py = a.dout, pz = a.q, pw = a.k, hz = hk, nz = a.HK;
   } else if (PASS == kLinSumFwd) {
-    px = nullptr, py = a.k, pz = a.v, hy = hk, ny = a.HK;
+    py = a.k, pz = a.v, hy = hk, ny = a.HK;
   } else {
-    px = nullptr, py = a.q, pz = a.dout, hy = hk, ny = a.HK;
+    py = a.q, pz = a.dout, hy = hk, ny = a.HK;
   }
   const float s_out = PASS == kLinFwd || PASS == kLinDq ? a.scale : 1.f;
   const float s_in = PT::kRev ? a.scale : 1.f;
@@ -274,7 +316,13 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
     col[t] = NT == 2 ? 32 * w + 8 * (c >> 2) + 4 * t + (c & 3) : 16 * w + c;
     colq[t] = NT == 2 ? 32 * w + 8 * (c & 3) + 4 * t : 16 * w + 4 * (c & 3);
   }
+  const int rowq = X::place(c, 4 * gq);  // a row operand's first element (rows 16 i + c)
   const int out_col = NT == 2 ? 32 * w + 8 * gq : 16 * w + 4 * gq;  // first column it stores
+
+  const bool per_k = PT::kDots && !a.out_f32;  // dq, dk of ungrouped heads
+  const int out_heads = per_k ? a.HK : a.H, out_head = per_k ? hk : h;
+  const int64_t out_size = PT::kDots && a.out_f32 ? 4 : (int64_t)sizeof(E);
+  const unsigned v_out = (unsigned)((c * out_heads * D + out_col) * out_size);
 
   f32x4 S[MT][NT];
   const float *src = nullptr;
@@ -303,39 +351,67 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
 
   uint4 sy[UPT], sz[UPT], sx[UPT], sw[UPT];  // the next chunk's rows
   float sg = 0.f;                            // ... log decays (wave 0)
+  // addresses: a uniform base per 256 units and one 32-bit offset per lane and row stride
+  const int r0 = tid / UPR, o0 = tid % UPR * EPU;
+  constexpr int kRows = 256 / UPR;  // rows per 256 units
+  const unsigned vx = (unsigned)((r0 * nx * D + o0) * sizeof(E)), vy = (unsigned)((r0 * ny * D + o0) * sizeof(E));
+  const unsigned vz = (unsigned)((r0 * nz * D + o0) * sizeof(E)), vw = (unsigned)((r0 * a.HK * D + o0) * sizeof(E));
+  const auto load16 = [](const void *base, int64_t elems, unsigned v) {
+    return *reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + elems * (int64_t)sizeof(E) + v);
+  };
   const auto fetch = [&](int ch) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
     const int n = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
+    const auto rows = [&](int u) {
+      const int64_t t = t0 + kRows * u;
+      sy[u] = load16(py, (t * ny + hy) * D, vy);
+      sz[u] = load16(pz, (t * nz + hz) * D, vz);
+      if (!PT::kSum) sx[u] = load16(px, (t * nx + hx) * D, vx);
+      if (PT::kDots) sw[u] = load16(pw, (t * a.HK + hk) * D, vw);
+    };
+    if (n == kChunk) {
 #pragma unroll
-    for (int u = 0; u < UPT; ++u) {
-      const int r = (tid + 256 * u) / UPR, o = (tid + 256 * u) % UPR * EPU;
-      const uint4 z = {0u, 0u, 0u, 0u};
-      sy[u] = sz[u] = sx[u] = sw[u] = z;
-      if (r < n) {
-        const int64_t t = t0 + r;
-        sy[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(py) + (t * ny + hy) * D + o);
-        sz[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(pz) + (t * nz + hz) * D + o);
-        if (!PT::kSum)
-          sx[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(px) + (t * nx + hx) * D + o);
-        if (PT::kDots)
-          sw[u] = *reinterpret_cast<const uint4 *>(static_cast<const E *>(pw) +
-                                                   (t * a.HK + hw) * D + o);
+      for (int u = 0; u < UPT; ++u) rows(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < UPT; ++u) {
+        sy[u] = sz[u] = sx[u] = sw[u] = uint4{0u, 0u, 0u, 0u};
+        if (r0 + kRows * u < n) rows(u);
       }
     }
-    if (w == 0) sg = lane < n ? a.g[a.g_head ? h : (t0 + lane) * a.H + h] : 0.f;
+    if (w == kDecayWave) sg = lane < n ? a.g[a.g_head ? h : (t0 + lane) * a.H + h] : 0.f;
+  };
+  // the decays of the chunk that was fetched (one wave), kept in registers until its tiles are up
+  F2 G{}, GC{}, total{0.f, 0.f};  // total: the unit's whole log decay
+  float from_start = 0.f, to_end = 0.f, near_a = 0.f, near_b = 0.f;
+  const auto make_decays = [&]() {
+    G = wave_scan2(log2_decay(sg));
+    GC = F2{__shfl(G.hi, 63, 64), __shfl(G.lo, 63, 64)};
+    from_start = exp2_fast(G.hi + G.lo);
+    to_end = exp2_fast((GC.hi - G.hi) + (GC.lo - G.lo));
+    if (!PT::kSum) {
+      // decay from the end of the 16-token tile before, and to the end of its own
+      const int e = lane | 15, b = e < 16 ? 0 : e - 16;
+      const F2 E1 = F2{__shfl(G.hi, e, 64), __shfl(G.lo, e, 64)};
+      const F2 B1 = F2{__shfl(G.hi, b, 64), __shfl(G.lo, b, 64)};
+      near_a = exp2_fast((G.hi - B1.hi) + (G.lo - B1.lo));
+      near_b = exp2_fast((E1.hi - G.hi) + (E1.lo - G.lo));
+    } else {
+      total = add2(total, GC);
+    }
   };
   // dg's parts of the chunk before (every wave's share is in LDS)
-  const auto flush_dots = [&](int ch) {
+  const auto flush_dots = [&](int ch, int par) {
     if (!PT::kDots || w != 1) return;
     const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
     float *const to = PASS == kLinDq ? a.dg_q : a.dg_k;
-    const float d = dots[0][lane] + dots[1][lane] + dots[2][lane] + dots[3][lane];
+    const float d = dots[par][0][lane] + dots[par][1][lane] + dots[par][2][lane] + dots[par][3][lane];
     if (t < t_end) to[t * a.H + h] = d;
     if (PASS == kLinDq) {
       // sum over the pairs s >= t > i = sum_{s >= t} (row sum - column sum); rows from the end
-      F2 x = F2{rsum[lane], 0.f};
+      F2 x = F2{rsum[par][lane], 0.f};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x = add2(x, F2{-csum[j][lane], 0.f});
+      for (int j = 0; j < 4; ++j) x = add2(x, F2{-csum[par][j][lane], 0.f});
       const F2 up = wave_scan2(x);
       const float th = __shfl(up.hi, 63, 64), tl = __shfl(up.lo, 63, 64);
       const F2 rest = add2(add2(F2{th, tl}, F2{-up.hi, -up.lo}), x);
@@ -343,39 +419,185 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
     }
   };
 
-  F2 total{0.f, 0.f};  // kSum: the unit's whole log decay (wave 0)
   const int step = PT::kRev ? -1 : 1;
   int ch = PT::kRev ? c1 - 1 : c0;
   const int nsteps = c1 - c0;
   // terms of the state update: three where the state is written out or feeds dg
   const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && a.final_state != nullptr));
-  if (nsteps > 0) fetch(ch);
+  if (nsteps > 0) {
+    fetch(ch);
+    if (w == kDecayWave) make_decays();
+  }
   for (int it = 0; it < nsteps; ++it, ch += step) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
     __syncthreads();
-    if (it > 0) flush_dots(ch - step);
+    const int par = it & 1;
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      const int o = (tid + 256 * u) / UPR * LD + (tid + 256 * u) % UPR * EPU;
+      const int o = (r0 + kRows * u) * LD + X::place(r0 + kRows * u, o0);
       *reinterpret_cast<uint4 *>(ty + o) = sy[u];
       *reinterpret_cast<uint4 *>(tz + o) = sz[u];
       if (!PT::kSum) *reinterpret_cast<uint4 *>(tx + o) = sx[u];
       if (PT::kDots) *reinterpret_cast<uint4 *>(tw + o) = sw[u];
     }
-    if (w == 0) {
-      const F2 G = wave_scan2(log2_decay(sg));
-      const F2 GC = F2{__shfl(G.hi, 63, 64), __shfl(G.lo, 63, 64)};
-      const float from_start = exp2_fast(G.hi + G.lo);
-      const float to_end = exp2_fast((GC.hi - G.hi) + (GC.lo - G.lo));
-      g_hi[lane] = G.hi;
-      g_lo[lane] = G.lo;
+    if (w == kDecayWave) {
       f_x[lane] = PT::kRev ? to_end : from_start;
       f_y[lane] = PT::kRev ? s_in * from_start : to_end;
+      if (!PT::kSum) {
+        g_hi[lane] = G.hi;
+        g_lo[lane] = G.lo;
+        f_a[lane] = near_a;
+        f_b[lane] = near_b;
+      }
       if (lane == 0) sh_decay = exp2_fast(GC.hi + GC.lo);
-      total = add2(total, GC);
     }
     __syncthreads();
-    if (it + 1 < nsteps) fetch(ch + step);
+    if (it > 0) flush_dots(ch - step, par ^ 1);
+    // the next chunk's loads: at once, or (four tiles) once the output's registers are free
+    if (!PT::kDots && it + 1 < nsteps) fetch(ch + step);
+
+    f32x4 o[4][NT];  // the output by 16-row tiles
+    if constexpr (!PT::kSum) {
+      // the pairs within the chunk: wave w forms P's tiles of its 16 rows of x
+      f32x4 p[4];
+      {
+        const int xr = 16 * w + c;
+        Frag xf[KS];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) xf[ks] = X::row(tx + xr * LD + rowq + 32 * ks);
+        const float xh = g_hi[xr], xl = g_lo[xr], x_near = PT::kRev ? f_b[xr] : f_a[xr];
+        // all four tiles of the row, so that every wave runs the same straight line of independent
+        // products; the tiles it does not need are dropped
+#pragma unroll
+        for (int yt = 0; yt < 4; ++yt) p[yt] = zero4();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int yt = 0; yt < 4; ++yt)
+            p[yt] = X::mma(X::row(ty + (16 * yt + c) * LD + rowq + 32 * ks), xf[ks], p[yt]);
+#pragma unroll
+        for (int yt = 0; yt < 4; ++yt) {
+          if (PT::kRev ? yt < w : yt > w) {
+            p[yt] = zero4();
+          } else if (yt != w) {
+            // e^{G_late - G_early} = to the end of the earlier tile, the tiles between, and from
+            // there: each factor at most one, no exponential per pair
+            const int e0 = 16 * (PT::kRev ? w : yt) + 15, e1 = 16 * (PT::kRev ? yt : w) - 1;
+            const float mid = exp2_fast((g_hi[e1] - g_hi[e0]) + (g_lo[e1] - g_lo[e0]));
+            const float fx = s_in * (x_near * mid);
+            const f32x4 fy = lds_f32x4((PT::kRev ? f_a : f_b) + 16 * yt + 4 * gq);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[yt][j] *= fx * fy[j];
+          } else {
+            const f32x4 yh = lds_f32x4(g_hi + 16 * yt + 4 * gq);
+            const f32x4 yl = lds_f32x4(g_lo + 16 * yt + 4 * gq);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int d = 4 * gq + j - c;
+              const float e = PT::kRev ? (yh[j] - xh) + (yl[j] - xl) : (xh - yh[j]) + (xl - yl[j]);
+              const bool in = PT::kRev ? d >= 0 : d <= 0;
+              p[yt][j] = in ? s_in * (p[yt][j] * exp2_fast(e)) : 0.f;
+            }
+          }
+        }
+        if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed
+          float r = 0.f;
+          Frag qf[KS];
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) qf[ks] = X::row(tw + xr * LD + rowq + 32 * ks);
+          f32x4 m[4];
+#pragma unroll
+          for (int yt = 0; yt < 4; ++yt) m[yt] = zero4();
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int yt = 0; yt < 4; ++yt)
+              m[yt] = X::mma(X::row(tz + (16 * yt + c) * LD + rowq + 32 * ks), qf[ks], m[yt]);
+#pragma unroll
+          for (int yt = 0; yt < 4; ++yt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool in = yt < w || (yt == w && 4 * gq + j < c);
+              const float x = in ? s_out * (m[yt][j] * p[yt][j]) : 0.f;
+              r += x;
+              const float cs = row16_sum_dpp(x);
+              if (c == 0) csum[par][w][16 * yt + 4 * gq + j] = cs;
+            }
+          }
+          r += __shfl_xor(r, 16, 64);
+          r += __shfl_xor(r, 32, 64);
+          if (gq == 0) rsum[par][xr] = r;
+        }
+      }
+      const auto store_p = [&]() {
+#pragma unroll
+        for (int yt = 0; yt < 4; ++yt) {
+          if (PT::kRev ? yt < (w & 2) : yt > (w | 1)) continue;
+          E *const to = tp + (p_slot<PT::kRev>(w, yt) * kPTerms * 64 + lane) * 4;
+          store4(to, p[yt]);
+          if (kPTerms == 2) {
+            f32x4 x = p[yt], unused = zero4();
+            X::residual(X::round(x, unused), x, unused);
+            store4(to + 256, x);
+          }
+        }
+      };
+      if (!PT::kDots) store_p();
+
+      // the state's share: 32 rows of the state at a time, split once for the four row tiles
+#pragma unroll
+      for (int xt = 0; xt < 4; ++xt)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[xt][t] = zero4();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        Frag sf[kStateTerms][NT], xf[4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          f32x4 s0 = S[2 * ks][t], s1 = S[2 * ks + 1][t];
+#pragma unroll
+          for (int i = 0; i < kStateTerms; ++i) {
+            sf[i][t] = X::round(s0, s1);
+            if (i + 1 < kStateTerms) X::residual(sf[i][t], s0, s1);
+          }
+        }
+#pragma unroll
+        for (int xt = 0; xt < 4; ++xt) {
+          xf[xt] = X::row(tx + (16 * xt + c) * LD + rowq + 32 * ks);
+        }
+#pragma unroll
+        for (int i = 0; i < kStateTerms; ++i)
+#pragma unroll
+          for (int xt = 0; xt < 4; ++xt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(sf[i][t], xf[xt], o[xt][t]);
+        sched_fence();
+      }
+#pragma unroll
+      for (int xt = 0; xt < 4; ++xt) {
+        const int xr = 16 * xt + c;
+        const float f = f_x[xr];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[xt][t] *= f;
+        if (PT::kDots) {  // x's share of dg: w . (the state's share of the output)
+          float d = 0.f;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const f32x4 wv = load4(tw + xr * LD + X::place(c, out_col) + 4 * t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d += wv[j] * o[xt][t][j];
+          }
+          d += __shfl_xor(d, 16, 64);
+          d += __shfl_xor(d, 32, 64);
+          if (gq == 0) dots[par][w][xr] = s_out * d;
+        }
+      }
+      lds_barrier();
+      if (PT::kDots) {
+        store_p();
+        lds_barrier();
+      }
+    }
 
     // z's columns of this wave: rows 32 kb + (order)
     Frag zf[2][NT];
@@ -388,104 +610,38 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
     if constexpr (!PT::kSum) {
       const int64_t n_rows = t_end - t0;
 #pragma unroll
-      for (int xt = 0; xt < 4; ++xt) {  // 16 output rows
-        const int xr = 16 * xt + c;
-        Frag xf[KS];
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) xf[ks] = X::row(tx + xr * LD + 32 * ks + 4 * gq);
-        f32x4 o[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {  // the state's share
-          o[t] = zero4();
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            o[t] = mma_split<E, kStateTerms, true>(S[2 * ks][t], S[2 * ks + 1][t], xf[ks], o[t]);
-          o[t] *= f_x[xr];
-        }
-        if (PT::kDots) {  // x's share of dg: w . (the state's share of the output)
-          float d = 0.f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const f32x4 wv = load4(tw + xr * LD + out_col + 4 * t);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d += wv[j] * o[t][j];
-          }
-          d += __shfl_xor(d, 16, 64);
-          d += __shfl_xor(d, 32, 64);
-          if (gq == 0) dots[w][xr] = s_out * d;
-        }
-        // the pairs within the chunk
-        f32x4 p[4];
-        const float xh = g_hi[xr], xl = g_lo[xr];
-#pragma unroll
-        for (int yt = 0; yt < 4; ++yt) {
-          p[yt] = zero4();
-          if (PT::kRev ? yt < xt : yt > xt) continue;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            p[yt] = X::mma(X::row(ty + (16 * yt + c) * LD + 32 * ks + 4 * gq), xf[ks], p[yt]);
-          const f32x4 yh = lds_f32x4(g_hi + 16 * yt + 4 * gq);
-          const f32x4 yl = lds_f32x4(g_lo + 16 * yt + 4 * gq);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int yr = 16 * yt + 4 * gq + j;
-            const float e = PT::kRev ? (yh[j] - xh) + (yl[j] - xl) : (xh - yh[j]) + (xl - yl[j]);
-            const bool in = yt != xt || (PT::kRev ? yr >= xr : yr <= xr);
-            p[yt][j] = in ? s_in * (p[yt][j] * exp2_fast(e)) : 0.f;
-          }
-        }
-        if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed, by wave xt
-          if (w == xt) {
-            float r = 0.f;
-            Frag qf[KS];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) qf[ks] = X::row(tw + xr * LD + 32 * ks + 4 * gq);
-#pragma unroll
-            for (int yt = 0; yt < 4; ++yt) {
-              f32x4 m = zero4();
-              if (yt <= xt) {
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                  m = X::mma(X::row(tz + (16 * yt + c) * LD + 32 * ks + 4 * gq), qf[ks], m);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool in = yt < xt || (yt == xt && 4 * gq + j < c);
-                const float x = in ? s_out * (m[j] * p[yt][j]) : 0.f;
-                r += x;
-                const float cs = row16_sum_dpp(x);
-                if (c == 0) csum[w][16 * yt + 4 * gq + j] = cs;
-              }
-            }
-            r += __shfl_xor(r, 16, 64);
-            r += __shfl_xor(r, 32, 64);
-            if (gq == 0) rsum[xr] = r;
-          }
-        }
+      for (int xt = 0; xt < 4; ++xt) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           if (PT::kRev ? 2 * kb + 1 < xt : 2 * kb > xt) continue;
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            o[t] = mma_split<E, kPTerms, false>(p[2 * kb], p[2 * kb + 1], zf[kb][t], o[t]);
-        }
-        if (xr < n_rows) {
-          const int64_t row = (t0 + xr) * (PT::kGrad && PASS != kLinDv && !a.out_f32 ? a.HK : a.H) +
-                              (PT::kGrad && PASS != kLinDv && !a.out_f32 ? hk : h);
+          for (int i = 0; i < kPTerms; ++i) {
+            const Frag pf = X::pair(tp + ((p_slot<PT::kRev>(xt, 2 * kb) * kPTerms + i) * 64 + lane) * 4,
+                                    kPTerms * 256);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) o[t] *= s_out;
+            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(zf[kb][t], pf, o[xt][t]);
+          }
+        }
+        const int xr = 16 * xt + c;
+        if (xr < n_rows) {
+          char *const base = static_cast<char *>(a.out) + ((t0 + 16 * xt) * out_heads + out_head) * D * out_size;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) o[xt][t] *= s_out;
           if (PT::kDots && a.out_f32) {
-            float *to = static_cast<float *>(a.out) + row * D + out_col;
-            if (NT == 2) store8(to, o[0], o[NT - 1]);
-            else store4(to, o[0]);
+            float *to = reinterpret_cast<float *>(base + v_out);
+            if (NT == 2) store8(to, o[xt][0], o[xt][NT - 1]);
+            else store4(to, o[xt][0]);
           } else {
-            E *to = static_cast<E *>(a.out) + row * D + out_col;
-            if (NT == 2) store8(to, o[0], o[NT - 1]);
-            else store4(to, o[0]);
+            E *to = reinterpret_cast<E *>(base + v_out);
+            if (NT == 2) store8(to, o[xt][0], o[xt][NT - 1]);
+            else store4(to, o[xt][0]);
           }
         }
       }
     }
+
+    sched_fence();
+    if (PT::kDots && it + 1 < nsteps) fetch(ch + step);
 
     // the state after the chunk
     const float decay = sh_decay;
@@ -502,29 +658,39 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
         f32x4 u = fa * X::lo_part(zf[kb][t]), v = fb * X::hi_part(zf[kb][t]);
         b1[t] = X::round(u, v);
         if constexpr (kB) {
-          u -= X::lo_part(b1[t]), v -= X::hi_part(b1[t]);
+          X::residual(b1[t], u, v);
           b2[t] = X::round(u, v);
-          u -= X::lo_part(b2[t]), v -= X::hi_part(b2[t]);
-          b3[t] = X::round(u, v);
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const Frag yf = X::template column<LD>(ty, 32 * kb, 16 * m + 4 * (c & 3), 16 * m + c, c, gq);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          S[m][t] = X::mma(yf, b1[t], S[m][t]);
-          if constexpr (kB) {
-            S[m][t] = X::mma(yf, b2[t], S[m][t]);
-            if (precise) S[m][t] = X::mma(yf, b3[t], S[m][t]);
+          if (precise) {
+            X::residual(b2[t], u, v);
+            b3[t] = X::round(u, v);
           }
         }
       }
+#pragma unroll
+      for (int m = 0; m < MT; m += 2) {
+        Frag yf[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          yf[i] = X::template column<LD>(ty, 32 * kb, 16 * (m + i) + 4 * (c & 3), 16 * (m + i) + c, c, gq);
+        const auto add = [&](const Frag(&b)[NT]) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S[m + i][t] = X::mma(yf[i], b[t], S[m + i][t]);
+        };
+        add(b1);
+        if constexpr (kB) {
+          add(b2);
+          if (precise) add(b3);
+        }
+      }
+      sched_fence();
     }
+    if (w == kDecayWave && it + 1 < nsteps) make_decays();
   }
   if (PT::kDots && nsteps > 0) {
     __syncthreads();
-    flush_dots(ch - step);
+    flush_dots(ch - step, (nsteps - 1) & 1);
   }
 
   const auto store_state = [&](float *to) {
@@ -537,7 +703,8 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
   };
   if (PT::kSum) {
     store_state((PT::kRev ? a.unit_r : a.unit_s) + uh * D * D);
-    if (tid == 0) a.unit_decay[(PT::kRev ? a.units * a.H : 0) + uh] = exp2_fast(total.hi + total.lo);
+    if (w == kDecayWave && lane == 0)
+      a.unit_decay[(PT::kRev ? a.units * a.H : 0) + uh] = exp2_fast(total.hi + total.lo);
   }
   if ((PASS == kLinFwd || PASS == kLinDv) && edge_out && a.final_state)
     store_state(a.final_state + ((int64_t)seq * a.H + h) * D * D);
@@ -559,9 +726,9 @@ __global__ __launch_bounds__(256) void lin_pass_kernel(LinArgs a) {
     }
     d = wave_sum_f64(d);
     __syncthreads();  // the last chunk's parts have been read
-    if (lane == 0) dots[w][0] = (float)d;
+    if (lane == 0) dots[0][w][0] = (float)d;
     __syncthreads();
-    if (tid == 0) a.unit_dot[uh] = dots[0][0] + dots[1][0] + dots[2][0] + dots[3][0];
+    if (tid == 0) a.unit_dot[uh] = dots[0][0][0] + dots[0][1][0] + dots[0][2][0] + dots[0][3][0];
   }
 }
 
@@ -707,7 +874,7 @@ __global__ __launch_bounds__(256) void lin_zero_kernel(float *x, int64_t n) {
 
 template <class E, int D, int PASS>
 hipError_t launch_pass(const LinArgs &a, hipStream_t stream) {
-  constexpr size_t lds = pass_tile_bytes<E, D, PASS>();
+  constexpr size_t lds = pass_lds_bytes<E, D, PASS>();
   if (lds > 65536) {  // above the default limit of dynamic LDS
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void *>(&lin_pass_kernel<E, D, PASS>),

@@ -60,6 +60,7 @@ gdn_status segment_chunks(const gdn_linattn_problem *p, int32_t *L) {
     if (slots == 0) {
       gdn_status s = device_info(&slots);
       if (s != GDN_OK) return s;
+      slots *= gdn::linattn_blocks_per_cu(p->head_dim, p->dtype == GDN_DTYPE_BF16);
     }
     const int64_t want = std::max<int64_t>(kMinSegment, ceil_div(nc * p->num_heads, slots));
     if (nc > 2 * want && (int64_t)p->num_seqs * p->num_heads < 2 * slots)
