@@ -44,6 +44,9 @@ struct LinArgs {
   int64_t T;
   int32_t N, H, HK, L;
   int64_t units;
+  // whole sequences (L = 0), at most kMaxLongestFirst: taken longest first, all heads of one before
+  // the next, so that the last workgroups to start are the shortest
+  int32_t longest_first;
   float scale;
 };
 

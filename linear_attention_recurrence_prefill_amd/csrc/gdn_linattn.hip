@@ -11,8 +11,8 @@
 // of L chunks exactly: a unit's own sum from zero (kLinSum*), the sums joined along the sequence
 // (lin_scan_kernel), the unit run from its true start.
 //
-// Work of one workgroup (256 threads, 4 waves): one (unit, head).  Wave w owns D / 4 columns of the
-// state, all D rows of them, in MFMA accumulators: in that layout (lane n + 16 (m / 4), item m % 4)
+// Work of one workgroup (4 waves): one (unit, head).  Wave w owns D / 4 columns of the state, all D
+// rows of them, in MFMA accumulators: in that layout (lane n + 16 (m / 4), item m % 4)
 // two stacked 16-row tiles are, as they stand, the operand of a 16x16x32 product over the rows, in
 // the row order {4 gq + j, 16 + 4 gq + j}.  All row operands are read in that order, so neither
 // the state nor the 64 x 64 products P ever pass through LDS, and waves meet only at the tile
@@ -36,6 +36,9 @@
 
 namespace gdn {
 namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinLog2 = -512.f;
 constexpr float kNoDecay = -150.f;  // 2^-150 rounds to zero in fp32
@@ -78,28 +81,36 @@ __device__ __forceinline__ F2 log2_decay(float g) {
 // the product itself, for both input types.
 template <class E>
 struct Op;
-// bf16 tiles: rows of D + 16 elements (8 (mod 64) banks apart), and in every other group of eight
-// rows the 16-byte units are exchanged in pairs.  The eight rows that a half wave's transposing
-// read takes then lie on different banks, and so do the sixteen rows of a row read.
+// bf16 tiles in LDS.  Tiles of which rows and columns are read (y, z): rows of D + 16 elements, 8
+// (mod 64) banks apart, with the 16-byte units exchanged in pairs in every other group of eight
+// rows, so that the eight rows of a transposing read's half wave lie on different banks.  Tiles of
+// which only rows are read (x, w): rows of D + 4 elements, whose 16 rows' 8-byte reads of one cycle
+// fill the 32 banks.
 template <>
 struct Op<bf16> {
   typedef bf16x8 Frag;
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  static constexpr int kPad = 16;
-  // where column `col` of row `row` is within the row (col in units that stay whole: 4 elements)
+  static constexpr int kPadYZ = 16, kPadXW = 4;
+  // where column `col` of row `row` of y or z is within the row (col a multiple of 4)
   static __device__ __forceinline__ int place(int row, int col) { return col ^ (row & 8); }
+  static __device__ __forceinline__ void put_xw(bf16 *p, u32x4 x) {  // 8-byte aligned
+    *reinterpret_cast<u32x2 *>(p) = __builtin_shufflevector(x, x, 0, 1);
+    *reinterpret_cast<u32x2 *>(p + 4) = __builtin_shufflevector(x, x, 2, 3);
+  }
   static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return mma_bf16(a, b, c); }
   // a row, from its element at index 4 gq on (a multiple of 32 further: the next products')
   static __device__ __forceinline__ Frag row(const bf16 *p) {
     return cat8(lds_bf16x4(p), lds_bf16x4(p + 16));
   }
-  // a column: rows row0 + (order) of column `col`; `colq` is the column this lane addresses
-  template <int LD>
-  static __device__ __forceinline__ Frag column(const bf16 *tile, int row0, int colq, int, int c,
-                                                int gq) {
+  // a column: rows row0 + (order) of the tile's column that the lane's offset `at` is for
+  // (colq: the first of the four columns that the lane addresses in the transposing read)
+  static __device__ __forceinline__ int column_base(int colq, int, int c, int gq, int ld) {
     const int r = 4 * gq + (c >> 2);
-    const bf16 *p = tile + (row0 + r) * LD + place(r, colq);
-    return cat8(lds_tr16(p), lds_tr16(p + 16 * LD));
+    return r * ld + place(r, colq);
+  }
+  template <int LD>
+  static __device__ __forceinline__ Frag column(const bf16 *tile, int at) {
+    return cat8(lds_tr16(tile + at), lds_tr16(tile + at + 16 * LD));
   }
   static __device__ __forceinline__ Frag round(f32x4 a, f32x4 b) { return to_bf16x8(a, b); }
   // a, b less what round() made of them: x - hi is one dot product with (-1, 0) or (0, -1).  The
@@ -136,8 +147,9 @@ struct F32x8 {
 template <>
 struct Op<float> {
   typedef F32x8 Frag;
-  static constexpr int kPad = 4;
+  static constexpr int kPadYZ = 4, kPadXW = 4;
   static __device__ __forceinline__ int place(int, int col) { return col; }
+  static __device__ __forceinline__ void put_xw(float *p, u32x4 x) { *reinterpret_cast<u32x4 *>(p) = x; }
   static __device__ __forceinline__ f32x4 mma(Frag x, Frag y, f32x4 c) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) c = mma_f32(x.a[j], y.a[j], c);
@@ -148,10 +160,12 @@ struct Op<float> {
   static __device__ __forceinline__ Frag row(const float *p) {
     return F32x8{lds_f32x4(p), lds_f32x4(p + 16)};
   }
+  static __device__ __forceinline__ int column_base(int, int col, int, int gq, int ld) {
+    return 4 * gq * ld + col;
+  }
   template <int LD>
-  static __device__ __forceinline__ Frag column(const float *tile, int row0, int, int col, int,
-                                                int gq) {
-    const float *p = tile + (row0 + 4 * gq) * LD + col;
+  static __device__ __forceinline__ Frag column(const float *tile, int at) {
+    const float *p = tile + at;
     F32x8 f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -179,14 +193,6 @@ template <>
 __device__ __forceinline__ void store4<bf16>(bf16 *p, f32x4 x) {
   *reinterpret_cast<bf16x4 *>(p) = to_bf16x4(x);
 }
-__device__ __forceinline__ void store8(float *p, f32x4 x, f32x4 y) {
-  store4(p, x);
-  store4(p + 4, y);
-}
-__device__ __forceinline__ void store8(bf16 *p, f32x4 x, f32x4 y) {
-  *reinterpret_cast<bf16x8 *>(p) = to_bf16x8(x, y);
-}
-
 __device__ __forceinline__ f32x4 load4(const bf16 *p) {
   const bf16x4 x = lds_bf16x4(p);
   return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
@@ -223,8 +229,8 @@ constexpr size_t p_bytes() {
 template <class E, int D, int PASS>
 constexpr size_t pass_lds_bytes() {
   typedef PassTraits<PASS> PT;
-  const size_t tile = (size_t)64 * (D + Op<E>::kPad) * sizeof(E);
-  return PT::kTiles * tile + (PT::kSum || PT::kDots ? 0 : p_bytes<E>());
+  const int elems = 2 * 64 * (D + Op<E>::kPadYZ) + (PT::kTiles - 2) * 64 * (D + Op<E>::kPadXW);
+  return elems * sizeof(E) + (PT::kSum || PT::kDots ? 0 : p_bytes<E>());
 }
 
 }  // namespace
@@ -234,8 +240,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   typedef Op<E> X;
   typedef typename X::Frag Frag;
   typedef PassTraits<PASS> PT;
-  constexpr int LD = D + X::kPad;
   constexpr int NT = D / 64;      // 16-column tiles of the state per wave
+  constexpr int LDY = D + X::kPadYZ, LDX = D + X::kPadXW;
   constexpr int MT = D / 16;      // 16-row tiles of the state
   constexpr int KS = D / 32;      // products over a row
   constexpr int EPU = 16 / (int)sizeof(E);
@@ -245,27 +251,31 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   constexpr bool kB = sizeof(E) == 2;
   constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);
   constexpr int kPTerms = p_terms<E>();
-  constexpr int kDecayWave = PT::kRev ? 3 : 0;  // the wave with the fewest tiles of P
+  constexpr int kDecayWave = 3;  // waves 0 to 2 form P
 
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  E *const ty = reinterpret_cast<E *>(smem);   // tiles [64][LD]: y, z, x, w
-  E *const tz = ty + 64 * LD;
-  E *const tx = tz + 64 * LD;
-  E *const tw = tx + 64 * LD;
+  E *const ty = reinterpret_cast<E *>(smem);   // tiles of 64 rows
+  E *const tz = ty + 64 * LDY;
+  E *const tx = tz + 64 * LDY;
+  E *const tw = tx + 64 * LDX;
   // P: behind the tiles, or (four tiles) over x, which is dead by then
-  E *const tp = PT::kDots ? tx : tx + 64 * LD;
-  __shared__ __attribute__((aligned(16))) float g_hi[64], g_lo[64], f_x[64], f_y[64], f_a[64], f_b[64];
-  __shared__ float sh_decay;
-  __shared__ float dots[2][4][64], rsum[2][64], csum[2][4][64];  // by the chunk's parity
+  E *const tp = PT::kDots ? tx : tx + 64 * LDX;
+  // the chunk's decays, by its parity: G (log2, hi + lo) and the factors of x's and y's rows
+  __shared__ __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
+  __shared__ float s_decay[2];
+  // dg's parts, by the chunk's parity; row and column sums of the pairs by the other side's half
+  __shared__ float dots[2][4][64], rsum[2][2][64], csum[2][2][64];
   __shared__ int sh_unit[4];
 
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, gq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = blockIdx.y, hk = h / (a.H / a.HK);
+  const int unit = a.longest_first ? blockIdx.y : blockIdx.x;
+  const int h = a.longest_first ? blockIdx.x : blockIdx.y;
+  const int hk = __builtin_amdgcn_readfirstlane(h / (a.H / a.HK));
 
   if (w == 0) {
     Unit un{};
-    const bool ok = find_unit(a.cu, a.N, a.T, a.L, blockIdx.x, false, lane, un);
+    const bool ok = find_unit(a.cu, a.N, a.T, a.L, unit, false, lane, un, a.longest_first != 0);
     if (lane == 0) {
       sh_unit[0] = ok ? un.seq : -1;
       sh_unit[1] = un.c0;
@@ -277,52 +287,56 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   const int c0 = __builtin_amdgcn_readfirstlane(sh_unit[1]);
   const int c1 = __builtin_amdgcn_readfirstlane(sh_unit[2]);
   if (seq < 0) return;
-  const int64_t t_beg = a.cu[seq], t_end = a.cu[seq + 1];
+  // uniform, and known to be: the rows' addresses are made of scalars
+  const int64_t t_beg = __builtin_amdgcn_readfirstlane(a.cu[seq]);
+  const int64_t t_end = __builtin_amdgcn_readfirstlane(a.cu[seq + 1]);
   if (t_beg < 0 || t_end < t_beg || t_end > a.T) return;
   const int nch = (int)((t_end - t_beg + kChunk - 1) / kChunk);
   const bool first = c0 == 0, last = c1 >= nch;
   const bool edge_in = PT::kRev ? last : first;    // the pass starts at the sequence's edge
   const bool edge_out = PT::kRev ? first : last;   // ... ends there
-  const int64_t uh = (int64_t)blockIdx.x * a.H + h;
+  // a whole sequence's index is the sequence, whatever the order they are taken in
+  const int64_t uh = (int64_t)(a.L > 0 ? unit : seq) * a.H + h;
   if (PT::kSum) {
-    if (PASS == kLinSumFwd && first && h == 0 && tid == 0) a.seq_unit[seq] = blockIdx.x;
+    if (PASS == kLinSumFwd && first && h == 0 && tid == 0) a.seq_unit[seq] = unit;
     if (edge_out) return;  // no unit follows
   }
 
-  // the rows of this pass
+  // the rows of this pass, and which of them are key heads'
+  constexpr bool kXk = PASS == kLinFwd || PASS == kLinDv, kYk = PT::kSum || kXk, kZk = PT::kDots;
   const void *px = nullptr, *py, *pz, *pw = nullptr;
-  int hx = h, hy = h, hz = h, nx = a.H, ny = a.H, nz = a.H;
   if (PASS == kLinFwd) {
-    px = a.q, py = a.k, pz = a.v, hx = hy = hk, nx = ny = a.HK;
+    px = a.q, py = a.k, pz = a.v;
   } else if (PASS == kLinDq) {
-    px = a.dout, py = a.v, pz = a.k, pw = a.q, hz = hk, nz = a.HK;
+    px = a.dout, py = a.v, pz = a.k, pw = a.q;
   } else if (PASS == kLinDv) {
-    px = a.k, py = a.q, pz = a.dout, hx = hy = hk, nx = ny = a.HK;
+    px = a.k, py = a.q, pz = a.dout;
   } else if (PASS == kLinDk) {
-    px = a.v, py = a.dout, pz = a.q, pw = a.k, hz = hk, nz = a.HK;
+    px = a.v, py = a.dout, pz = a.q, pw = a.k;
   } else if (PASS == kLinSumFwd) {
-    py = a.k, pz = a.v, hy = hk, ny = a.HK;
+    py = a.k, pz = a.v;
   } else {
-    py = a.q, pz = a.dout, hy = hk, ny = a.HK;
+    py = a.q, pz = a.dout;
   }
-  const float s_out = PASS == kLinFwd || PASS == kLinDq ? a.scale : 1.f;
-  const float s_in = PT::kRev ? a.scale : 1.f;
+  const float s_out = PASS == kLinFwd || PASS == kLinDq ? a.scale : 1.f;  // of the state's share
+  const float s_p = a.scale;                                              // of P
+  const float s_y = PT::kRev ? a.scale : 1.f;                             // of what enters the state
 
-  // this wave's columns of the state: tile t's column of lane c, and the column that lane c
-  // addresses in a transposing read
-  int col[NT], colq[NT];
+  // this wave's columns of the state: tile t's column of lane c, and the first column that the
+  // lane addresses in a transposing read; in an output tile the lane has columns out_col + 4 t ..
+  int col[NT], z_at[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     col[t] = NT == 2 ? 32 * w + 8 * (c >> 2) + 4 * t + (c & 3) : 16 * w + c;
-    colq[t] = NT == 2 ? 32 * w + 8 * (c & 3) + 4 * t : 16 * w + 4 * (c & 3);
+    z_at[t] = X::column_base(NT == 2 ? 32 * w + 8 * (c & 3) + 4 * t : 16 * w + 4 * (c & 3), col[t], c, gq, LDY);
   }
-  const int rowq = X::place(c, 4 * gq);  // a row operand's first element (rows 16 i + c)
-  const int out_col = NT == 2 ? 32 * w + 8 * gq : 16 * w + 4 * gq;  // first column it stores
+  const int y_at = X::column_base(4 * (c & 3), c, c, gq, LDY);
+  const int out_col = NT == 2 ? 32 * w + 8 * gq : 16 * w + 4 * gq;
+  const int row_y = X::place(c, 4 * gq);    // a row operand's first element in y or z (rows 16 i + c)
 
   const bool per_k = PT::kDots && !a.out_f32;  // dq, dk of ungrouped heads
   const int out_heads = per_k ? a.HK : a.H, out_head = per_k ? hk : h;
-  const int64_t out_size = PT::kDots && a.out_f32 ? 4 : (int64_t)sizeof(E);
-  const unsigned v_out = (unsigned)((c * out_heads * D + out_col) * out_size);
+  const int v_out = c * out_heads * D + out_col;
 
   f32x4 S[MT][NT];
   const float *src = nullptr;
@@ -349,69 +363,68 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
       }
     }
 
-  uint4 sy[UPT], sz[UPT], sx[UPT], sw[UPT];  // the next chunk's rows
-  float sg = 0.f;                            // ... log decays (wave 0)
-  // addresses: a uniform base per 256 units and one 32-bit offset per lane and row stride
+  u32x4 sy[UPT], sz[UPT], sx[UPT], sw[UPT];  // the next chunk's rows
+  float sg = 0.f;                            // ... log decays (one wave)
+  // Rows are read and written through buffer resources of the chunk's rows: the base is scalar, a
+  // lane holds one 32-bit offset per row stride, and rows past the sequence's end are out of the
+  // buffer's range, so they read as zeros and are not written.
   const int r0 = tid / UPR, o0 = tid % UPR * EPU;
-  constexpr int kRows = 256 / UPR;  // rows per 256 units
-  const unsigned vx = (unsigned)((r0 * nx * D + o0) * sizeof(E)), vy = (unsigned)((r0 * ny * D + o0) * sizeof(E));
-  const unsigned vz = (unsigned)((r0 * nz * D + o0) * sizeof(E)), vw = (unsigned)((r0 * a.HK * D + o0) * sizeof(E));
-  const auto load16 = [](const void *base, int64_t elems, unsigned v) {
-    return *reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + elems * (int64_t)sizeof(E) + v);
+  constexpr int kRows = 256 / UPR;  // rows per round
+  const auto rows_of = [&](const void *base, int64_t t0, int heads, int head, int n, int size) {
+    const char *p = static_cast<const char *>(base) + (t0 * heads + head) * D * size;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0,
+                                             ((n - 1) * heads + 1) * D * size, 0x00020000);
+  };
+  // the lane's offset in the first round's rows, per row stride
+  const int vh = (r0 * a.H * D + o0) * (int)sizeof(E), vk = (r0 * a.HK * D + o0) * (int)sizeof(E);
+  const auto load_rows = [&](u32x4(&to)[UPT], const void *base, int64_t t0, bool of_k, int n) {
+    const int heads = of_k ? a.HK : a.H;
+    const auto rsrc = rows_of(base, t0, heads, of_k ? hk : h, n, sizeof(E));
+    int at = of_k ? vk : vh;
+    asm("" : "+v"(at));  // the rounds' offsets are made here, not kept
+#pragma unroll
+    for (int u = 0; u < UPT; ++u)
+      to[u] = __builtin_amdgcn_raw_buffer_load_b128(
+          rsrc, at + kRows * u * heads * D * (int)sizeof(E), 0, 0);
   };
   const auto fetch = [&](int ch) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
     const int n = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
-    const auto rows = [&](int u) {
-      const int64_t t = t0 + kRows * u;
-      sy[u] = load16(py, (t * ny + hy) * D, vy);
-      sz[u] = load16(pz, (t * nz + hz) * D, vz);
-      if (!PT::kSum) sx[u] = load16(px, (t * nx + hx) * D, vx);
-      if (PT::kDots) sw[u] = load16(pw, (t * a.HK + hk) * D, vw);
-    };
-    if (n == kChunk) {
-#pragma unroll
-      for (int u = 0; u < UPT; ++u) rows(u);
-    } else {
-#pragma unroll
-      for (int u = 0; u < UPT; ++u) {
-        sy[u] = sz[u] = sx[u] = sw[u] = uint4{0u, 0u, 0u, 0u};
-        if (r0 + kRows * u < n) rows(u);
-      }
-    }
+    load_rows(sy, py, t0, kYk, n);
+    load_rows(sz, pz, t0, kZk, n);
+    if (!PT::kSum) load_rows(sx, px, t0, kXk, n);
+    if (PT::kDots) load_rows(sw, pw, t0, true, n);
     if (w == kDecayWave) sg = lane < n ? a.g[a.g_head ? h : (t0 + lane) * a.H + h] : 0.f;
   };
-  // the decays of the chunk that was fetched (one wave), kept in registers until its tiles are up
-  F2 G{}, GC{}, total{0.f, 0.f};  // total: the unit's whole log decay
-  float from_start = 0.f, to_end = 0.f, near_a = 0.f, near_b = 0.f;
-  const auto make_decays = [&]() {
-    G = wave_scan2(log2_decay(sg));
-    GC = F2{__shfl(G.hi, 63, 64), __shfl(G.lo, 63, 64)};
-    from_start = exp2_fast(G.hi + G.lo);
-    to_end = exp2_fast((GC.hi - G.hi) + (GC.lo - G.lo));
-    if (!PT::kSum) {
-      // decay from the end of the 16-token tile before, and to the end of its own
-      const int e = lane | 15, b = e < 16 ? 0 : e - 16;
-      const F2 E1 = F2{__shfl(G.hi, e, 64), __shfl(G.lo, e, 64)};
-      const F2 B1 = F2{__shfl(G.hi, b, 64), __shfl(G.lo, b, 64)};
-      near_a = exp2_fast((G.hi - B1.hi) + (G.lo - B1.lo));
-      near_b = exp2_fast((E1.hi - G.hi) + (E1.lo - G.lo));
-    } else {
+  // the decays of the chunk that was fetched (one wave)
+  F2 total{0.f, 0.f};  // the unit's whole log decay
+  const auto make_decays = [&](int par) {
+    const F2 G = wave_scan2(log2_decay(sg));
+    const F2 GC = F2{__shfl(G.hi, 63, 64), __shfl(G.lo, 63, 64)};
+    const float from_start = exp2_fast(G.hi + G.lo);
+    const float to_end = exp2_fast((GC.hi - G.hi) + (GC.lo - G.lo));
+    s_x[par][lane] = s_out * (PT::kRev ? to_end : from_start);
+    s_yf[par][lane] = PT::kRev ? s_y * from_start : to_end;
+    if (lane == 0) s_decay[par] = exp2_fast(GC.hi + GC.lo);
+    if (PT::kSum) {
       total = add2(total, GC);
+    } else {
+      s_hi[par][lane] = G.hi;
+      s_lo[par][lane] = G.lo;
     }
   };
   // dg's parts of the chunk before (every wave's share is in LDS)
   const auto flush_dots = [&](int ch, int par) {
-    if (!PT::kDots || w != 1) return;
+    if (!PT::kDots || w != kDecayWave) return;
     const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
     float *const to = PASS == kLinDq ? a.dg_q : a.dg_k;
     const float d = dots[par][0][lane] + dots[par][1][lane] + dots[par][2][lane] + dots[par][3][lane];
     if (t < t_end) to[t * a.H + h] = d;
     if (PASS == kLinDq) {
       // sum over the pairs s >= t > i = sum_{s >= t} (row sum - column sum); rows from the end
-      F2 x = F2{rsum[par][lane], 0.f};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x = add2(x, F2{-csum[par][j][lane], 0.f});
+      const float r1 = lane >= 32 ? rsum[par][1][lane] : 0.f, c0 = lane < 32 ? csum[par][0][lane] : 0.f;
+      const F2 x = add2(add2(F2{rsum[par][0][lane], 0.f}, F2{r1, 0.f}),
+                        add2(F2{-c0, 0.f}, F2{-csum[par][1][lane], 0.f}));
       const F2 up = wave_scan2(x);
       const float th = __shfl(up.hi, 63, 64), tl = __shfl(up.lo, 63, 64);
       const F2 rest = add2(add2(F2{th, tl}, F2{-up.hi, -up.lo}), x);
@@ -426,151 +439,153 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && a.final_state != nullptr));
   if (nsteps > 0) {
     fetch(ch);
-    if (w == kDecayWave) make_decays();
+    if (w == kDecayWave) make_decays(0);
   }
   for (int it = 0; it < nsteps; ++it, ch += step) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
-    __syncthreads();
     const int par = it & 1;
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      const int o = (r0 + kRows * u) * LD + X::place(r0 + kRows * u, o0);
-      *reinterpret_cast<uint4 *>(ty + o) = sy[u];
-      *reinterpret_cast<uint4 *>(tz + o) = sz[u];
-      if (!PT::kSum) *reinterpret_cast<uint4 *>(tx + o) = sx[u];
-      if (PT::kDots) *reinterpret_cast<uint4 *>(tw + o) = sw[u];
-    }
-    if (w == kDecayWave) {
-      f_x[lane] = PT::kRev ? to_end : from_start;
-      f_y[lane] = PT::kRev ? s_in * from_start : to_end;
-      if (!PT::kSum) {
-        g_hi[lane] = G.hi;
-        g_lo[lane] = G.lo;
-        f_a[lane] = near_a;
-        f_b[lane] = near_b;
-      }
-      if (lane == 0) sh_decay = exp2_fast(GC.hi + GC.lo);
+      const int row = r0 + kRows * u, oy = row * LDY + X::place(row, o0), ox = row * LDX + o0;
+      *reinterpret_cast<u32x4 *>(ty + oy) = sy[u];
+      *reinterpret_cast<u32x4 *>(tz + oy) = sz[u];
+      if (!PT::kSum) X::put_xw(tx + ox, sx[u]);
+      if (PT::kDots) X::put_xw(tw + ox, sw[u]);
     }
     __syncthreads();
+    const float *const g_hi = s_hi[par], *const g_lo = s_lo[par], *const f_x = s_x[par], *const f_y = s_yf[par];
     if (it > 0) flush_dots(ch - step, par ^ 1);
-    // the next chunk's loads: at once, or (four tiles) once the output's registers are free
+    // the next chunk's loads: at once, or (four tiles) once the first half's registers are free
     if (!PT::kDots && it + 1 < nsteps) fetch(ch + step);
+
+    Frag zf[2][NT];  // z's columns of this wave: rows 32 kb + (order)
+    const auto read_z = [&]() {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) zf[kb][t] = X::template column<LDY>(tz + 32 * kb * LDY, z_at[t]);
+    };
+    if constexpr (PT::kSum) read_z();
 
     f32x4 o[4][NT];  // the output by 16-row tiles
     if constexpr (!PT::kSum) {
-      // the pairs within the chunk: wave w forms P's tiles of its 16 rows of x
-      f32x4 p[4];
-      {
-        const int xr = 16 * w + c;
-        Frag xf[KS];
+      // the pairs within the chunk: P by 32 x 32 blocks, three of them (the fourth is masked), one
+      // for each of waves 0 to 2
+      const int xb = PT::kRev ? w >> 1 : (w + 1) >> 1, yb = PT::kRev ? (w + 1) >> 1 : w >> 1;
+      f32x4 p[2][2];
+      if (w < 3) {
+        const E *const xrow = tx + (32 * xb + c) * LDX + 4 * gq, *const yrow = ty + (32 * yb + c) * LDY + row_y;
+        float xh[2], xl[2];
+        f32x4 yh[2], yl[2];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) xf[ks] = X::row(tx + xr * LD + rowq + 32 * ks);
-        const float xh = g_hi[xr], xl = g_lo[xr], x_near = PT::kRev ? f_b[xr] : f_a[xr];
-        // all four tiles of the row, so that every wave runs the same straight line of independent
-        // products; the tiles it does not need are dropped
-#pragma unroll
-        for (int yt = 0; yt < 4; ++yt) p[yt] = zero4();
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int yt = 0; yt < 4; ++yt)
-            p[yt] = X::mma(X::row(ty + (16 * yt + c) * LD + rowq + 32 * ks), xf[ks], p[yt]);
-#pragma unroll
-        for (int yt = 0; yt < 4; ++yt) {
-          if (PT::kRev ? yt < w : yt > w) {
-            p[yt] = zero4();
-          } else if (yt != w) {
-            // e^{G_late - G_early} = to the end of the earlier tile, the tiles between, and from
-            // there: each factor at most one, no exponential per pair
-            const int e0 = 16 * (PT::kRev ? w : yt) + 15, e1 = 16 * (PT::kRev ? yt : w) - 1;
-            const float mid = exp2_fast((g_hi[e1] - g_hi[e0]) + (g_lo[e1] - g_lo[e0]));
-            const float fx = s_in * (x_near * mid);
-            const f32x4 fy = lds_f32x4((PT::kRev ? f_a : f_b) + 16 * yt + 4 * gq);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[yt][j] *= fx * fy[j];
-          } else {
-            const f32x4 yh = lds_f32x4(g_hi + 16 * yt + 4 * gq);
-            const f32x4 yl = lds_f32x4(g_lo + 16 * yt + 4 * gq);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = 4 * gq + j - c;
-              const float e = PT::kRev ? (yh[j] - xh) + (yl[j] - xl) : (xh - yh[j]) + (xl - yl[j]);
-              const bool in = PT::kRev ? d >= 0 : d <= 0;
-              p[yt][j] = in ? s_in * (p[yt][j] * exp2_fast(e)) : 0.f;
-            }
-          }
+        for (int i = 0; i < 2; ++i) {
+          xh[i] = g_hi[32 * xb + 16 * i + c], xl[i] = g_lo[32 * xb + 16 * i + c];
+          yh[i] = lds_f32x4(g_hi + 32 * yb + 16 * i + 4 * gq);
+          yl[i] = lds_f32x4(g_lo + 32 * yb + 16 * i + 4 * gq);
+          p[i][0] = p[i][1] = zero4();
         }
-        if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed
-          float r = 0.f;
-          Frag qf[KS];
+        const auto block = [&](const E *xr, const E *yr, f32x4(&acc)[2][2]) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) qf[ks] = X::row(tw + xr * LD + rowq + 32 * ks);
-          f32x4 m[4];
+          for (int ks = 0; ks < KS; ++ks) {
+            const Frag x0 = X::row(xr + 32 * ks), x1 = X::row(xr + 16 * LDX + 32 * ks);
+            const Frag y0 = X::row(yr + 32 * ks), y1 = X::row(yr + 16 * LDY + 32 * ks);
+            acc[0][0] = X::mma(y0, x0, acc[0][0]);
+            acc[0][1] = X::mma(y1, x0, acc[0][1]);
+            acc[1][0] = X::mma(y0, x1, acc[1][0]);
+            acc[1][1] = X::mma(y1, x1, acc[1][1]);
+          }
+        };
+        block(xrow, yrow, p);
 #pragma unroll
-          for (int yt = 0; yt < 4; ++yt) m[yt] = zero4();
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int yt = 0; yt < 4; ++yt)
-              m[yt] = X::mma(X::row(tz + (16 * yt + c) * LD + rowq + 32 * ks), qf[ks], m[yt]);
-#pragma unroll
-          for (int yt = 0; yt < 4; ++yt) {
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const bool in = yt < w || (yt == w && 4 * gq + j < c);
-              const float x = in ? s_out * (m[yt][j] * p[yt][j]) : 0.f;
-              r += x;
-              const float cs = row16_sum_dpp(x);
-              if (c == 0) csum[par][w][16 * yt + 4 * gq + j] = cs;
+              const int d = 32 * (yb - xb) + 16 * (k - i) + 4 * gq + j - c;  // y's token less x's
+              const bool in = PT::kRev ? d >= 0 : d <= 0;
+              const float e = PT::kRev ? (yh[k][j] - xh[i]) + (yl[k][j] - xl[i])
+                                       : (xh[i] - yh[k][j]) + (xl[i] - yl[k][j]);
+              const float v = s_p * (p[i][k][j] * exp2_fast(in ? e : 0.f));
+              p[i][k][j] = in ? v : 0.f;
             }
+        if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed
+          f32x4 m[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) m[i][0] = m[i][1] = zero4();
+          sched_fence();
+          block(tw + (32 * xb + c) * LDX + 4 * gq, tz + (32 * yb + c) * LDY + row_y, m);
+          float r[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float cs = 0.f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const bool in = 32 * (yb - xb) + 16 * (k - i) + 4 * gq + j - c < 0;
+                const float x = in ? m[i][k][j] * p[i][k][j] : 0.f;
+                r[i] += x;
+                cs += x;
+              }
+              cs = row16_sum_dpp(cs);
+              if (c == 0) csum[par][xb][32 * yb + 16 * k + 4 * gq + j] = cs;
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            r[i] += __shfl_xor(r[i], 16, 64);
+            r[i] += __shfl_xor(r[i], 32, 64);
+            if (gq == 0) rsum[par][yb][32 * xb + 16 * i + c] = r[i];
           }
-          r += __shfl_xor(r, 16, 64);
-          r += __shfl_xor(r, 32, 64);
-          if (gq == 0) rsum[par][xr] = r;
         }
       }
       const auto store_p = [&]() {
+        if (w < 3) {
 #pragma unroll
-        for (int yt = 0; yt < 4; ++yt) {
-          if (PT::kRev ? yt < (w & 2) : yt > (w | 1)) continue;
-          E *const to = tp + (p_slot<PT::kRev>(w, yt) * kPTerms * 64 + lane) * 4;
-          store4(to, p[yt]);
-          if (kPTerms == 2) {
-            f32x4 x = p[yt], unused = zero4();
-            X::residual(X::round(x, unused), x, unused);
-            store4(to + 256, x);
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              E *const to = tp + (p_slot<PT::kRev>(2 * xb + i, 2 * yb + k) * kPTerms * 64 + lane) * 4;
+              store4(to, p[i][k]);
+              if (kPTerms == 2) {
+                f32x4 x = p[i][k], unused = zero4();
+                X::residual(X::round(x, unused), x, unused);
+                store4(to + 256, x);
+              }
+            }
         }
       };
       if (!PT::kDots) store_p();
 
-      // the state's share: 32 rows of the state at a time, split once for the four row tiles
+      // the state's share: 32 rows of the state at a time, split once for the four row tiles, with
+      // the next 32 rows' operands read during the products
 #pragma unroll
       for (int xt = 0; xt < 4; ++xt)
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[xt][t] = zero4();
+      Frag xf[2][4];
+      const auto read_x = [&](int ks) {
+#pragma unroll
+        for (int xt = 0; xt < 4; ++xt) xf[ks & 1][xt] = X::row(tx + (16 * xt + c) * LDX + 32 * ks + 4 * gq);
+      };
+      sched_fence();
+      read_x(0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        Frag sf[kStateTerms][NT], xf[4];
+        if (ks + 1 < KS) read_x(ks + 1);
+        f32x4 s0[NT], s1[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          f32x4 s0 = S[2 * ks][t], s1 = S[2 * ks + 1][t];
-#pragma unroll
-          for (int i = 0; i < kStateTerms; ++i) {
-            sf[i][t] = X::round(s0, s1);
-            if (i + 1 < kStateTerms) X::residual(sf[i][t], s0, s1);
-          }
-        }
-#pragma unroll
-        for (int xt = 0; xt < 4; ++xt) {
-          xf[xt] = X::row(tx + (16 * xt + c) * LD + rowq + 32 * ks);
-        }
+        for (int t = 0; t < NT; ++t) s0[t] = S[2 * ks][t], s1[t] = S[2 * ks + 1][t];
 #pragma unroll
         for (int i = 0; i < kStateTerms; ++i)
 #pragma unroll
-          for (int xt = 0; xt < 4; ++xt)
+          for (int t = 0; t < NT; ++t) {
+            const Frag sf = X::round(s0[t], s1[t]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(sf[i][t], xf[xt], o[xt][t]);
+            for (int xt = 0; xt < 4; ++xt) o[xt][t] = X::mma(sf, xf[ks & 1][xt], o[xt][t]);
+            if (i + 1 < kStateTerms) X::residual(sf, s0[t], s1[t]);
+          }
         sched_fence();
       }
 #pragma unroll
@@ -583,68 +598,79 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
           float d = 0.f;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const f32x4 wv = load4(tw + xr * LD + X::place(c, out_col) + 4 * t);
+            const f32x4 wv = load4(tw + xr * LDX + out_col + 4 * t);
 #pragma unroll
             for (int j = 0; j < 4; ++j) d += wv[j] * o[xt][t][j];
           }
           d += __shfl_xor(d, 16, 64);
           d += __shfl_xor(d, 32, 64);
-          if (gq == 0) dots[par][w][xr] = s_out * d;
+          if (gq == 0) dots[par][w][xr] = d;
         }
       }
+      read_z();
       lds_barrier();
       if (PT::kDots) {
         store_p();
+        if (it + 1 < nsteps) fetch(ch + step);
         lds_barrier();
       }
-    }
 
-    // z's columns of this wave: rows 32 kb + (order)
-    Frag zf[2][NT];
+      // the pairs' share, by 32 rows of y and term; the next operands are read during the products
+      Frag pf[2][4];
+      const auto needed = [](int kb, int xt) { return PT::kRev ? 2 * kb + 1 >= xt : 2 * kb <= xt; };
+      const auto read_p = [&](int g) {
+        const int kb = g / kPTerms, i = g % kPTerms;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        zf[kb][t] = X::template column<LD>(tz, 32 * kb, colq[t], col[t], c, gq);
-
-    if constexpr (!PT::kSum) {
-      const int64_t n_rows = t_end - t0;
-#pragma unroll
-      for (int xt = 0; xt < 4; ++xt) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          if (PT::kRev ? 2 * kb + 1 < xt : 2 * kb > xt) continue;
-#pragma unroll
-          for (int i = 0; i < kPTerms; ++i) {
-            const Frag pf = X::pair(tp + ((p_slot<PT::kRev>(xt, 2 * kb) * kPTerms + i) * 64 + lane) * 4,
+        for (int xt = 0; xt < 4; ++xt)
+          if (needed(kb, xt))
+            pf[g & 1][xt] = X::pair(tp + ((p_slot<PT::kRev>(xt, 2 * kb) * kPTerms + i) * 64 + lane) * 4,
                                     kPTerms * 256);
+      };
+      read_p(0);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(zf[kb][t], pf, o[xt][t]);
-          }
-        }
-        const int xr = 16 * xt + c;
-        if (xr < n_rows) {
-          char *const base = static_cast<char *>(a.out) + ((t0 + 16 * xt) * out_heads + out_head) * D * out_size;
+      for (int g = 0; g < 2 * kPTerms; ++g) {
+        if (g + 1 < 2 * kPTerms) read_p(g + 1);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) o[xt][t] *= s_out;
-          if (PT::kDots && a.out_f32) {
-            float *to = reinterpret_cast<float *>(base + v_out);
-            if (NT == 2) store8(to, o[xt][0], o[xt][NT - 1]);
-            else store4(to, o[xt][0]);
-          } else {
-            E *to = reinterpret_cast<E *>(base + v_out);
-            if (NT == 2) store8(to, o[xt][0], o[xt][NT - 1]);
-            else store4(to, o[xt][0]);
-          }
-        }
+        for (int xt = 0; xt < 4; ++xt)
+          if (needed(g / kPTerms, xt))
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(zf[g / kPTerms][t], pf[g & 1][xt], o[xt][t]);
+        sched_fence();
       }
     }
 
-    sched_fence();
-    if (PT::kDots && it + 1 < nsteps) fetch(ch + step);
+    // the state after the chunk: by 32 rows of y and z, two 16-row tiles of the state at a time
+    const float decay = s_decay[par];
+    Frag yf[2][2];
+    const auto read_y = [&](int g) {
+      const int kb = g / (MT / 2), m = g % (MT / 2) * 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        yf[g & 1][i] = X::template column<LDY>(ty + 32 * kb * LDY + 16 * (m + i), y_at);
+    };
+    read_y(0);
 
-    // the state after the chunk
-    const float decay = sh_decay;
+    if constexpr (!PT::kSum) {
+      const bool f32_out = PT::kDots && a.out_f32;
+      const int n_rows = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
+      const auto rsrc = rows_of(a.out, t0, out_heads, out_head, n_rows, f32_out ? 4 : (int)sizeof(E));
+      int v_row = v_out;
+      asm("" : "+v"(v_row));
+#pragma unroll
+      for (int xt = 0; xt < 4; ++xt) {
+        const int at = v_row + 16 * xt * out_heads * D;
+        if (f32_out || !kB) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[xt][t]), rsrc, (at + 4 * t) * 4, 0, 0);
+        } else if (NT == 2) {
+          __builtin_amdgcn_raw_buffer_store_b128(
+              __builtin_bit_cast(u32x4, to_bf16x8(o[xt][0], o[xt][NT - 1])), rsrc, at * 2, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, to_bf16x4(o[xt][0])), rsrc, at * 2, 0, 0);
+        }
+      }
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -667,26 +693,24 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
         }
       }
 #pragma unroll
-      for (int m = 0; m < MT; m += 2) {
-        Frag yf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          yf[i] = X::template column<LD>(ty, 32 * kb, 16 * (m + i) + 4 * (c & 3), 16 * (m + i) + c, c, gq);
+      for (int mm = 0; mm < MT / 2; ++mm) {
+        const int g = kb * (MT / 2) + mm, m = 2 * mm;
+        if (g + 1 < MT) read_y(g + 1);
         const auto add = [&](const Frag(&b)[NT]) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) S[m + i][t] = X::mma(yf[i], b[t], S[m + i][t]);
+            for (int t = 0; t < NT; ++t) S[m + i][t] = X::mma(yf[g & 1][i], b[t], S[m + i][t]);
         };
         add(b1);
         if constexpr (kB) {
           add(b2);
           if (precise) add(b3);
         }
+        sched_fence();
       }
-      sched_fence();
     }
-    if (w == kDecayWave && it + 1 < nsteps) make_decays();
+    if (w == kDecayWave && it + 1 < nsteps) make_decays(par ^ 1);
   }
   if (PT::kDots && nsteps > 0) {
     __syncthreads();
@@ -881,8 +905,8 @@ hipError_t launch_pass(const LinArgs &a, hipStream_t stream) {
         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lin_pass_kernel<E, D, PASS>), dim3((unsigned)a.units, a.H), dim3(256), lds,
-                     stream, a);
+  hipLaunchKernelGGL((lin_pass_kernel<E, D, PASS>), a.longest_first ? dim3(a.H, (unsigned)a.units) : dim3((unsigned)a.units, a.H),
+                     dim3(256), lds, stream, a);
   return hipGetLastError();
 }
 

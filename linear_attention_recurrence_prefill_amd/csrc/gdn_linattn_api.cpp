@@ -131,6 +131,7 @@ gdn::LinArgs base_args(const gdn_linattn_problem *p, const Layout &l, const void
   a.HK = k_heads(p);
   a.L = l.L;
   a.units = l.units;
+  a.longest_first = l.L == 0 && p->num_seqs > 1 && p->num_seqs <= gdn::kMaxLongestFirst;
   a.scale = p->scale;
   if (l.L > 0) {
     a.unit_s = reinterpret_cast<float *>(ws + l.unit_s);
