@@ -28,9 +28,9 @@ struct LinArgs {
   const float *h0;       // initial states, or null
   int64_t h0_stride;
   const float *dht;      // gradients of the final states [N, H, D, D], or null
-  void *out;             // o, dq, dk or dv
-  int32_t out_f32;       // dq, dk as fp32 per value head (grouped heads)
-  float *final_state;    // ht or dh0 per sequence [N, H, D, D], or null
+  void *o, *dq, *dk, *dv;
+  int32_t grad_f32;      // dq, dk as fp32 per value head [T, H, D] (grouped heads)
+  float *ht, *dh0;       // per sequence [N, H, D, D], or null
   // split runs (L > 0): per unit and head, the states at the unit's start (unit_s) and the state
   // gradients at its end (unit_r), [units, H, D, D]; before the scan they hold the unit's own
   // contribution, with its whole decay in decay_s (decay_r: the same for the reversed sums)
@@ -52,11 +52,10 @@ struct LinArgs {
 
 // Workgroups of the passes that one CU holds at once (registers and LDS).
 inline int linattn_blocks_per_cu(int D, bool bf16) { return bf16 || D == 64 ? 2 : 1; }
-hipError_t launch_linattn_pass(const LinArgs &a, int D, bool bf16, LinPass pass, hipStream_t stream);
-// The states at the units' starts (rev: the state gradients at their ends) from the units' sums.
-hipError_t launch_linattn_scan(const LinArgs &a, int D, bool rev, hipStream_t stream);
-// dg from its parts (and its sum over the tokens with g_head).
-hipError_t launch_linattn_dg(const LinArgs &a, hipStream_t stream);
+// The forward: the units' sums and the states at their starts (split runs), then the output.
+hipError_t launch_linattn_fwd(const LinArgs &a, int D, bool bf16, hipStream_t stream);
+// The backward: the same in both directions, dq, dk, dv and dg's parts, then dg.
+hipError_t launch_linattn_bwd(const LinArgs &a, int D, bool bf16, hipStream_t stream);
 // out[t, hk] = sum over the H / HK value heads of part[t, h], fp32 to the input type.
 hipError_t launch_linattn_group_sum(const float *part, int64_t T, int32_t H, int32_t HK, int32_t D,
                                     bool bf16, void *out, hipStream_t stream);

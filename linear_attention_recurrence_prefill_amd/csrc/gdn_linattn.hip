@@ -41,6 +41,7 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinLog2 = -512.f;
+constexpr int kShortUnit = 4;        // chunks
 constexpr float kNoDecay = -150.f;  // 2^-150 rounds to zero in fp32
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLog2eLo = 1.925963033500e-8f;  // log2(e) - kLog2e
@@ -235,8 +236,17 @@ constexpr size_t pass_lds_bytes() {
 
 }  // namespace
 
+struct PassShared {
+  // the chunk's decays, by its parity: G (log2, hi + lo) and the factors of x's and y's rows
+  __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
+  // dg's parts, by the chunk's parity; row and column sums of the pairs by the other side's half
+  float dots[2][4][64], rsum[2][2][64], csum[2][2][64];
+  float s_decay[2];
+  int unit[4];
+};
+
 template <class E, int D, int PASS>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(LinArgs a) {
+__device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShared &sh) {
   typedef Op<E> X;
   typedef typename X::Frag Frag;
   typedef PassTraits<PASS> PT;
@@ -249,23 +259,21 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   constexpr int UPT = 64 * UPR / 256;     // ... per thread and tile
   // terms of the split operands (see the file's head)
   constexpr bool kB = sizeof(E) == 2;
-  constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);
+  constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);  // ... at most, see state_terms
   constexpr int kPTerms = p_terms<E>();
   constexpr int kDecayWave = 3;  // waves 0 to 2 form P
 
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   E *const ty = reinterpret_cast<E *>(smem);   // tiles of 64 rows
   E *const tz = ty + 64 * LDY;
   E *const tx = tz + 64 * LDY;
   E *const tw = tx + 64 * LDX;
   // P: behind the tiles, or (four tiles) over x, which is dead by then
   E *const tp = PT::kDots ? tx : tx + 64 * LDX;
-  // the chunk's decays, by its parity: G (log2, hi + lo) and the factors of x's and y's rows
-  __shared__ __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
-  __shared__ float s_decay[2];
-  // dg's parts, by the chunk's parity; row and column sums of the pairs by the other side's half
-  __shared__ float dots[2][4][64], rsum[2][2][64], csum[2][2][64];
-  __shared__ int sh_unit[4];
+  auto &s_hi = sh.s_hi, &s_lo = sh.s_lo, &s_x = sh.s_x, &s_yf = sh.s_yf;
+  auto &dots = sh.dots;
+  auto &rsum = sh.rsum, &csum = sh.csum;
+  auto &s_decay = sh.s_decay;
+  auto &sh_unit = sh.unit;
 
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, gq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -334,7 +342,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   const int out_col = NT == 2 ? 32 * w + 8 * gq : 16 * w + 4 * gq;
   const int row_y = X::place(c, 4 * gq);    // a row operand's first element in y or z (rows 16 i + c)
 
-  const bool per_k = PT::kDots && !a.out_f32;  // dq, dk of ungrouped heads
+  void *const out = PASS == kLinFwd ? a.o : PASS == kLinDq ? a.dq : PASS == kLinDk ? a.dk : a.dv;
+  float *const final_state = PASS == kLinFwd ? a.ht : PASS == kLinDv ? a.dh0 : nullptr;
+  const bool f32_out = PT::kDots && a.grad_f32;   // dq, dk of grouped heads: fp32 per value head
+  const bool per_k = PT::kDots && !f32_out;
   const int out_heads = per_k ? a.HK : a.H, out_head = per_k ? hk : h;
   const int v_out = c * out_heads * D + out_col;
 
@@ -436,7 +447,12 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   int ch = PT::kRev ? c1 - 1 : c0;
   const int nsteps = c1 - c0;
   // terms of the state update: three where the state is written out or feeds dg
-  const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && a.final_state != nullptr));
+  const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && final_state != nullptr));
+  // Terms of the state in the outputs o and dv: one in longer units.  Its rounding, 2^-9 of each
+  // element, adds to the output's own of the same size (1.65e-3 becomes at most 2.3e-3 in the mean
+  // square) and takes a tenth off the pass (200K tokens x 16 heads: 0.90 to 0.81 ms); in units of a
+  // few chunks, which wait for memory and each other anyway, it would cost accuracy for nothing.
+  const int state_terms = PT::kDots || nsteps <= kShortUnit ? kStateTerms : 1;
   if (nsteps > 0) {
     fetch(ch);
     if (w == kDecayWave) make_decays(0);
@@ -564,28 +580,32 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
       for (int xt = 0; xt < 4; ++xt)
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[xt][t] = zero4();
-      Frag xf[2][4];
+      constexpr int XB = PT::kDots ? 1 : 2;  // sets of operands (four tiles leave registers for one)
+      Frag xf[XB][4];
       const auto read_x = [&](int ks) {
 #pragma unroll
-        for (int xt = 0; xt < 4; ++xt) xf[ks & 1][xt] = X::row(tx + (16 * xt + c) * LDX + 32 * ks + 4 * gq);
+        for (int xt = 0; xt < 4; ++xt) xf[ks % XB][xt] = X::row(tx + (16 * xt + c) * LDX + 32 * ks + 4 * gq);
       };
       sched_fence();
       read_x(0);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        if (ks + 1 < KS) read_x(ks + 1);
+        if (XB == 2 && ks + 1 < KS) read_x(ks + 1);
+        if (XB == 1 && ks > 0) read_x(ks);
         f32x4 s0[NT], s1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) s0[t] = S[2 * ks][t], s1[t] = S[2 * ks + 1][t];
 #pragma unroll
-        for (int i = 0; i < kStateTerms; ++i)
+        for (int i = 0; i < kStateTerms; ++i) {
+          if (i > 0 && i >= state_terms) break;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const Frag sf = X::round(s0[t], s1[t]);
 #pragma unroll
-            for (int xt = 0; xt < 4; ++xt) o[xt][t] = X::mma(sf, xf[ks & 1][xt], o[xt][t]);
+            for (int xt = 0; xt < 4; ++xt) o[xt][t] = X::mma(sf, xf[ks % XB][xt], o[xt][t]);
             if (i + 1 < kStateTerms) X::residual(sf, s0[t], s1[t]);
           }
+        }
         sched_fence();
       }
 #pragma unroll
@@ -616,25 +636,26 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
       }
 
       // the pairs' share, by 32 rows of y and term; the next operands are read during the products
-      Frag pf[2][4];
+      Frag pf[XB][4];
       const auto needed = [](int kb, int xt) { return PT::kRev ? 2 * kb + 1 >= xt : 2 * kb <= xt; };
       const auto read_p = [&](int g) {
         const int kb = g / kPTerms, i = g % kPTerms;
 #pragma unroll
         for (int xt = 0; xt < 4; ++xt)
           if (needed(kb, xt))
-            pf[g & 1][xt] = X::pair(tp + ((p_slot<PT::kRev>(xt, 2 * kb) * kPTerms + i) * 64 + lane) * 4,
+            pf[g % XB][xt] = X::pair(tp + ((p_slot<PT::kRev>(xt, 2 * kb) * kPTerms + i) * 64 + lane) * 4,
                                     kPTerms * 256);
       };
       read_p(0);
 #pragma unroll
       for (int g = 0; g < 2 * kPTerms; ++g) {
-        if (g + 1 < 2 * kPTerms) read_p(g + 1);
+        if (XB == 2 && g + 1 < 2 * kPTerms) read_p(g + 1);
+        if (XB == 1 && g > 0) read_p(g);
 #pragma unroll
         for (int xt = 0; xt < 4; ++xt)
           if (needed(g / kPTerms, xt))
 #pragma unroll
-            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(zf[g / kPTerms][t], pf[g & 1][xt], o[xt][t]);
+            for (int t = 0; t < NT; ++t) o[xt][t] = X::mma(zf[g / kPTerms][t], pf[g % XB][xt], o[xt][t]);
         sched_fence();
       }
     }
@@ -651,9 +672,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
     read_y(0);
 
     if constexpr (!PT::kSum) {
-      const bool f32_out = PT::kDots && a.out_f32;
       const int n_rows = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
-      const auto rsrc = rows_of(a.out, t0, out_heads, out_head, n_rows, f32_out ? 4 : (int)sizeof(E));
+      const auto rsrc = rows_of(out, t0, out_heads, out_head, n_rows, f32_out ? 4 : (int)sizeof(E));
       int v_row = v_out;
       asm("" : "+v"(v_row));
 #pragma unroll
@@ -730,8 +750,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
     if (w == kDecayWave && lane == 0)
       a.unit_decay[(PT::kRev ? a.units * a.H : 0) + uh] = exp2_fast(total.hi + total.lo);
   }
-  if ((PASS == kLinFwd || PASS == kLinDv) && edge_out && a.final_state)
-    store_state(a.final_state + ((int64_t)seq * a.H + h) * D * D);
+  if ((PASS == kLinFwd || PASS == kLinDv) && edge_out && final_state)
+    store_state(final_state + ((int64_t)seq * a.H + h) * D * D);
   if (PASS == kLinDq) {  // <state, its gradient> at the unit's end
     const float *ds = last ? (a.dht ? a.dht + ((int64_t)seq * a.H + h) * D * D : nullptr)
                            : a.unit_r + uh * D * D;
@@ -756,17 +776,51 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_pass_kernel(L
   }
 }
 
+// One pass, or (GROUP) the passes of one stage of the backward side by side: grid z picks it.
+// kGroupSums: the units' sums in both directions; kGroupGrads: dq, dk, dv.
+enum { kGroupSums = 16, kGroupGrads };
+
+template <class E, int D, int WHAT>
+constexpr size_t stage_lds_bytes() {
+  if constexpr (WHAT == kGroupSums) {
+    return pass_lds_bytes<E, D, kLinSumFwd>();
+  } else if constexpr (WHAT == kGroupGrads) {
+    return std::max(pass_lds_bytes<E, D, kLinDq>(), pass_lds_bytes<E, D, kLinDv>());
+  } else {
+    return pass_lds_bytes<E, D, WHAT>();
+  }
+}
+
+template <class E, int D, int WHAT>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_stage_kernel(LinArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  __shared__ PassShared sh;
+  if constexpr (WHAT == kGroupSums) {
+    if (blockIdx.z == 0) lin_pass<E, D, kLinSumFwd>(a, smem, sh);
+    else lin_pass<E, D, kLinSumRev>(a, smem, sh);
+  } else if constexpr (WHAT == kGroupGrads) {
+    if (blockIdx.z == 0) lin_pass<E, D, kLinDq>(a, smem, sh);
+    else if (blockIdx.z == 1) lin_pass<E, D, kLinDk>(a, smem, sh);
+    else lin_pass<E, D, kLinDv>(a, smem, sh);
+  } else {
+    lin_pass<E, D, WHAT>(a, smem, sh);
+  }
+}
+
 namespace {
 
 // The states at the units' starts from the units' own sums, in place: along each sequence of more
 // than one unit, S <- decay_u S + sum_u, written where unit u + 1's sum was.  rev: the gradients at
-// the units' ends, from the last unit to the first.  One thread per four elements of a state; the
-// loads run kAhead units ahead of the chain.
-constexpr int kAhead = 4;
+// the units' ends, from the last unit to the first.  One thread per two elements of a state, its
+// loads kAhead units ahead of the chain: a chain's step is two instructions, so the time is that of
+// the bytes in flight (32K tokens x 8 heads, 57 units: 33 us with 4 units of 16 bytes ahead).
+constexpr int kAhead = 16;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 template <bool REV>
-__global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
+__device__ __forceinline__ void lin_scan(const LinArgs &a, int D, int64_t e) {
   const int seq = blockIdx.x, h = blockIdx.y;
-  const int64_t e = ((int64_t)blockIdx.z * 256 + threadIdx.x) * 4, DD = (int64_t)D * D;
+  const int64_t DD = (int64_t)D * D;
   const int32_t b0 = a.cu[seq], b1 = a.cu[seq + 1];
   if (b0 < 0 || b1 < b0 || b1 > a.T || e >= DD) return;
   const int nch = (b1 - b0 + kChunk - 1) / kChunk, nu = (nch + a.L - 1) / a.L;
@@ -776,20 +830,20 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
   const int64_t row = (int64_t)a.H * DD;
   float *const st = (REV ? a.unit_r : a.unit_s) + u0 * row + h * DD + e;
   const float *const dec = a.unit_decay + (REV ? a.units * a.H : 0) + u0 * a.H + h;
-  f32x4 S = zero4();
+  f32x2 S = {0.f, 0.f};
   const float *init = REV ? (a.dht ? a.dht + ((int64_t)seq * a.H + h) * DD + e : nullptr)
                           : (a.h0 ? a.h0 + seq * a.h0_stride + h * DD + e : nullptr);
-  if (init) S = *reinterpret_cast<const f32x4 *>(init);
+  if (init) S = *reinterpret_cast<const f32x2 *>(init);
   // step s passes unit us(s) and writes the state to unit us(s + 1), whose sum was read kAhead
   // steps before its own step, so always before that write
   const int steps = nu - 1;
   const auto us = [&](int s) { return REV ? nu - 1 - s : s; };
-  f32x4 b[kAhead];
+  f32x2 b[kAhead];
   float d[kAhead];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) {
     const int s = min(j, steps - 1);
-    b[j] = *reinterpret_cast<const f32x4 *>(st + us(s) * row);
+    b[j] = *reinterpret_cast<const f32x2 *>(st + us(s) * row);
     d[j] = dec[(int64_t)us(s) * a.H];
   }
   for (int s0 = 0; s0 < steps; s0 += kAhead) {
@@ -799,72 +853,101 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
       if (s < steps) {
         S = d[j] * S + b[j];
         if (s + kAhead < steps) {
-          b[j] = *reinterpret_cast<const f32x4 *>(st + us(s + kAhead) * row);
+          b[j] = *reinterpret_cast<const f32x2 *>(st + us(s + kAhead) * row);
           d[j] = dec[(int64_t)us(s + kAhead) * a.H];
         }
-        *reinterpret_cast<f32x4 *>(st + us(s + 1) * row) = S;
+        *reinterpret_cast<f32x2 *>(st + us(s + 1) * row) = S;
       }
     }
   }
+}
+
+// grid z: D^2 / 512 pieces of the states, then (both directions) as many of the state gradients
+__global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
+  const int pieces = D * D / 512, z = blockIdx.z;
+  const int64_t e = ((int64_t)(z < pieces ? z : z - pieces) * 256 + threadIdx.x) * 2;
+  if (z < pieces) lin_scan<false>(a, D, e);
+  else lin_scan<true>(a, D, e);
 }
 
 // dg_t = <dS_t, e^{g_t} S_{t-1}> from its parts: the pairs within the chunk on both sides of t,
 // and the scan of q . dq and k . dk (the states' shares) from the unit's end, where
 // <S, dS> is known: sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S, dS>_end.  The pairs' part has
 // no cancelling terms; the scan's terms are of the size of dg near them, and it restarts at every
-// unit's end.  One wave per (unit, head), from the unit's last chunk to its first.  A token whose
+// unit's end.  One workgroup per (unit, head), from the unit's end by blocks of 64 chunks: the waves
+// sum their chunks side by side, then finish them with the sums of the later ones.  A token whose
 // decay is zero in fp32 has no gradient.
 __global__ __launch_bounds__(256) void lin_dg_kernel(LinArgs a) {
-  const int lane = threadIdx.x & 63, h = blockIdx.y * 4 + (threadIdx.x >> 6);
-  if (h >= a.H) return;
+  __shared__ double sums[64], part[4];
+  __shared__ int sh_unit[3];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = blockIdx.y;
   const int64_t uh = (int64_t)blockIdx.x * a.H + h;
-  Unit un{};
-  bool ok = find_unit(a.cu, a.N, a.T, a.L, blockIdx.x, false, lane, un);
-  int64_t t_beg = 0, t_end = 0;
-  if (ok) {
-    t_beg = a.cu[un.seq], t_end = a.cu[un.seq + 1];
-    ok = t_beg >= 0 && t_end >= t_beg && t_end <= a.T && un.c1 > un.c0;
+  if (w == 0) {
+    Unit un{};
+    const bool ok = find_unit(a.cu, a.N, a.T, a.L, blockIdx.x, false, lane, un);
+    if (lane == 0) {
+      sh_unit[0] = ok ? un.seq : -1;
+      sh_unit[1] = un.c0;
+      sh_unit[2] = un.c1;
+    }
   }
-  double sum = 0.0;
+  __syncthreads();
+  const int seq = sh_unit[0], c0 = sh_unit[1], c1 = sh_unit[2];
+  const int64_t t_beg = seq < 0 ? 0 : a.cu[seq], t_end = seq < 0 ? 0 : a.cu[seq + 1];
+  const bool ok = seq >= 0 && t_beg >= 0 && t_end >= t_beg && t_end <= a.T && c1 > c0;
+  double total = 0.0;
   if (ok) {
     double b = (double)a.unit_dot[uh];
     const float gh = a.g_head ? a.g[h] : 0.f;
-    struct Part {
-      float q, k, p, g;
-    };
-    const auto fetch = [&](int ch) {
-      const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
-      Part x{0.f, 0.f, 0.f, 0.f};
-      if (t < t_end) {
-        const int64_t i = t * a.H + h;
-        x.q = a.dg_q[i], x.k = a.dg_k[i], x.p = a.dg_pairs[i];
-        x.g = a.g_head ? gh : a.g[i];
+    for (int hi = c1; hi > c0; hi -= 64) {  // chunks [lo, hi)
+      const int lo = max(c0, hi - 64), n = hi - lo;
+#pragma unroll 4
+      for (int j = w; j < n; j += 4) {
+        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane, i = t * a.H + h;
+        const double s = wave_sum_f64(t < t_end ? (double)a.dg_q[i] - (double)a.dg_k[i] : 0.0);
+        if (lane == 0) sums[j] = s;
       }
-      return x;
-    };
-    Part next = fetch(un.c1 - 1);
-    for (int ch = un.c1 - 1; ch >= un.c0; --ch) {
-      const Part x = next;
-      if (ch > un.c0) next = fetch(ch - 1);
-      double s = (double)x.q - (double)x.k;  // sum over the lanes from this one on
+      __syncthreads();
+      // the sums of the chunks after each one, within the block
+      double after = 0.0, all = 0.0;
+      {
+        const double x = lane < n ? sums[lane] : 0.0;
+        double s = x;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_down(s, off, 64);
-        if (lane + off < 64) s += y;
+        for (int off = 1; off < 64; off <<= 1) {
+          const double y = __shfl_down(s, off, 64);
+          if (lane + off < 64) s += y;
+        }
+        after = s - x;
+        all = __shfl(s, 0, 64);
       }
-      const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
-      const F2 lg = log2_decay(x.g);
-      const double dg = lg.hi <= kNoDecay ? 0.0 : (double)x.p + s + b;
-      if (t < t_end) {
-        if (!a.g_head) a.dg[t * a.H + h] = (float)dg;
-        sum += dg;
+#pragma unroll 2
+      for (int j = w; j < n; j += 4) {
+        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane, i = t * a.H + h;
+        const bool in = t < t_end;
+        double s = in ? (double)a.dg_q[i] - (double)a.dg_k[i] : 0.0;  // from this lane on
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const double y = __shfl_down(s, off, 64);
+          if (lane + off < 64) s += y;
+        }
+        const double from_end = b + __shfl(after, j, 64);
+        if (in) {
+          const F2 lg = log2_decay(a.g_head ? gh : a.g[i]);
+          const double dg = lg.hi <= kNoDecay ? 0.0 : (double)a.dg_pairs[i] + s + from_end;
+          if (!a.g_head) a.dg[i] = (float)dg;
+          total += dg;
+        }
       }
-      b += __shfl(s, 0, 64);
+      b += all;
+      __syncthreads();
     }
   }
   if (a.g_head) {
-    sum = wave_sum_f64(sum);
-    if (lane == 0) a.dg_unit[uh] = sum;
+    total = wave_sum_f64(total);
+    if (lane == 0) part[w] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) a.dg_unit[uh] = part[0] + part[1] + part[2] + part[3];
   }
 }
 
@@ -896,53 +979,56 @@ __global__ __launch_bounds__(256) void lin_zero_kernel(float *x, int64_t n) {
     x[i] = 0.f;
 }
 
-template <class E, int D, int PASS>
-hipError_t launch_pass(const LinArgs &a, hipStream_t stream) {
-  constexpr size_t lds = pass_lds_bytes<E, D, PASS>();
+template <class E, int D, int WHAT>
+hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
+  constexpr size_t lds = stage_lds_bytes<E, D, WHAT>();
+  constexpr int kinds = WHAT == kGroupSums ? 2 : WHAT == kGroupGrads ? 3 : 1;
+  const void *kernel = reinterpret_cast<const void *>(&lin_stage_kernel<E, D, WHAT>);
   if (lds > 65536) {  // above the default limit of dynamic LDS
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(&lin_pass_kernel<E, D, PASS>),
-        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((lin_pass_kernel<E, D, PASS>), a.longest_first ? dim3(a.H, (unsigned)a.units) : dim3((unsigned)a.units, a.H),
-                     dim3(256), lds, stream, a);
+  const unsigned u = (unsigned)a.units, h = (unsigned)a.H;
+  hipLaunchKernelGGL((lin_stage_kernel<E, D, WHAT>),
+                     a.longest_first ? dim3(h, u, kinds) : dim3(u, h, kinds), dim3(256), lds, stream, a);
   return hipGetLastError();
 }
 
-template <class E, int D>
-hipError_t launch_pass_of(const LinArgs &a, LinPass pass, hipStream_t stream) {
-  switch (pass) {
-    case kLinFwd: return launch_pass<E, D, kLinFwd>(a, stream);
-    case kLinDq: return launch_pass<E, D, kLinDq>(a, stream);
-    case kLinDv: return launch_pass<E, D, kLinDv>(a, stream);
-    case kLinDk: return launch_pass<E, D, kLinDk>(a, stream);
-    case kLinSumFwd: return launch_pass<E, D, kLinSumFwd>(a, stream);
-    default: return launch_pass<E, D, kLinSumRev>(a, stream);
-  }
+template <int WHAT>
+hipError_t launch_stage_of(const LinArgs &a, int D, bool is_bf16, hipStream_t stream) {
+  if (D == 128)
+    return is_bf16 ? launch_stage<bf16, 128, WHAT>(a, stream) : launch_stage<float, 128, WHAT>(a, stream);
+  return is_bf16 ? launch_stage<bf16, 64, WHAT>(a, stream) : launch_stage<float, 64, WHAT>(a, stream);
+}
+
+hipError_t launch_scan(const LinArgs &a, int D, int directions, hipStream_t stream) {
+  hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)a.N, a.H, directions * (D * D / 512)), dim3(256), 0,
+                     stream, a, D);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linattn_pass(const LinArgs &a, int D, bool is_bf16, LinPass pass,
-                               hipStream_t stream) {
-  if (D == 128)
-    return is_bf16 ? launch_pass_of<bf16, 128>(a, pass, stream)
-                   : launch_pass_of<float, 128>(a, pass, stream);
-  return is_bf16 ? launch_pass_of<bf16, 64>(a, pass, stream)
-                 : launch_pass_of<float, 64>(a, pass, stream);
+hipError_t launch_linattn_fwd(const LinArgs &a, int D, bool is_bf16, hipStream_t stream) {
+  if (a.L > 0) {
+    hipError_t e = launch_stage_of<kLinSumFwd>(a, D, is_bf16, stream);
+    if (e == hipSuccess) e = launch_scan(a, D, 1, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_stage_of<kLinFwd>(a, D, is_bf16, stream);
 }
 
-hipError_t launch_linattn_scan(const LinArgs &a, int D, bool rev, hipStream_t stream) {
-  const dim3 grid((unsigned)a.N, a.H, D * D / 1024);
-  if (rev) hipLaunchKernelGGL(lin_scan_kernel<true>, grid, dim3(256), 0, stream, a, D);
-  else hipLaunchKernelGGL(lin_scan_kernel<false>, grid, dim3(256), 0, stream, a, D);
-  return hipGetLastError();
-}
-
-hipError_t launch_linattn_dg(const LinArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL(lin_dg_kernel, dim3((unsigned)a.units, (a.H + 3) / 4), dim3(256), 0, stream, a);
-  hipError_t e = hipGetLastError();
+hipError_t launch_linattn_bwd(const LinArgs &a, int D, bool is_bf16, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (a.L > 0) {
+    e = launch_stage_of<kGroupSums>(a, D, is_bf16, stream);
+    if (e == hipSuccess) e = launch_scan(a, D, 2, stream);
+    if (e != hipSuccess) return e;
+  }
+  e = launch_stage_of<kGroupGrads>(a, D, is_bf16, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(lin_dg_kernel, dim3((unsigned)a.units, a.H), dim3(256), 0, stream, a);
+  e = hipGetLastError();
   if (e != hipSuccess || !a.g_head) return e;
   hipLaunchKernelGGL(lin_dg_head_kernel, dim3(a.H), dim3(256), 0, stream, a);
   return hipGetLastError();

@@ -227,15 +227,10 @@ gdn_status gdn_linattn_fwd(const gdn_linattn_problem *p, const void *q, const vo
     if (s != GDN_OK) return s;
   }
   gdn::LinArgs a = base_args(p, l, q, k, v, g, cu_seqlens, h0, static_cast<char *>(workspace));
-  a.out = o;
-  a.final_state = ht;
-  const bool bf = p->dtype == GDN_DTYPE_BF16;
-  const int D = p->head_dim;
-  if (l.L > 0) {
-    LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinSumFwd, stream), "linear attention: unit sums");
-    LAUNCH(gdn::launch_linattn_scan(a, D, false, stream), "linear attention: unit states");
-  }
-  LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinFwd, stream), "linear attention forward");
+  a.o = o;
+  a.ht = ht;
+  LAUNCH(gdn::launch_linattn_fwd(a, p->head_dim, p->dtype == GDN_DTYPE_BF16, stream),
+         "linear attention forward");
   return after(stream);
 }
 
@@ -294,25 +289,14 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
   if (p->head_decay) a.dg_unit = reinterpret_cast<double *>(ws + l.dg_unit);
   a.dg = dg;
   const bool bf = p->dtype == GDN_DTYPE_BF16, grouped = k_heads(p) != p->num_heads;
-  if (l.L > 0) {
-    LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinSumFwd, stream), "linear attention: unit sums");
-    LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinSumRev, stream),
-           "linear attention: unit gradient sums");
-    LAUNCH(gdn::launch_linattn_scan(a, D, false, stream), "linear attention: unit states");
-    LAUNCH(gdn::launch_linattn_scan(a, D, true, stream), "linear attention: unit gradients");
-  }
   float *const dq_part = grouped ? reinterpret_cast<float *>(ws + l.dq_part) : nullptr;
   float *const dk_part = grouped ? reinterpret_cast<float *>(ws + l.dk_part) : nullptr;
-  a.out_f32 = grouped;
-  a.out = grouped ? dq_part : dq;
-  LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinDq, stream), "linear attention: dq");
-  a.out = grouped ? dk_part : dk;
-  LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinDk, stream), "linear attention: dk");
-  a.out_f32 = 0;
-  a.out = dv;
-  a.final_state = dh0 && shared ? reinterpret_cast<float *>(ws + l.dh0_seq) : dh0;
-  LAUNCH(gdn::launch_linattn_pass(a, D, bf, gdn::kLinDv, stream), "linear attention: dv");
-  LAUNCH(gdn::launch_linattn_dg(a, stream), "linear attention: dg");
+  a.grad_f32 = grouped;
+  a.dq = grouped ? dq_part : dq;
+  a.dk = grouped ? dk_part : dk;
+  a.dv = dv;
+  a.dh0 = dh0 && shared ? reinterpret_cast<float *>(ws + l.dh0_seq) : dh0;
+  LAUNCH(gdn::launch_linattn_bwd(a, D, bf, stream), "linear attention backward");
   if (grouped) {
     LAUNCH(gdn::launch_linattn_group_sum(dq_part, T, p->num_heads, k_heads(p), D, bf, dq, stream),
            "linear attention: dq of shared heads");
@@ -320,7 +304,7 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
            "linear attention: dk of shared heads");
   }
   if (dh0 && shared)
-    LAUNCH(gdn::launch_sum_dh0(a.final_state, p->num_seqs, p->num_heads, D, dh0, stream),
+    LAUNCH(gdn::launch_sum_dh0(a.dh0, p->num_seqs, p->num_heads, D, dh0, stream),
            "linear attention: dh0 of a shared state");
   return after(stream);
 }
