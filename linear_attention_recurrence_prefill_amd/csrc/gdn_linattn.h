@@ -36,7 +36,7 @@ struct LinArgs {
   // contribution, with its whole decay in decay_s (decay_r: the same for the reversed sums)
   float *unit_s, *unit_r, *unit_decay;
   int32_t *seq_unit;     // [N]: each sequence's first unit
-  // dg's parts: pairs within a chunk, q . dq and k . dk of the states' shares, [T, H] each, and
+  // dg's parts: pairs within a chunk, q . dq and k . dk of the states' shares, [H, T] each, and
   // <state, state gradient> at each unit's end, [units, H]
   float *dg_pairs, *dg_q, *dg_k, *unit_dot;
   double *dg_unit;       // with g_head: dg summed over each unit, [units, H]

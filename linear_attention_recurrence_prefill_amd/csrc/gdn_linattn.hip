@@ -200,6 +200,12 @@ __device__ __forceinline__ f32x4 load4(const bf16 *p) {
 }
 __device__ __forceinline__ f32x4 load4(const float *p) { return lds_f32x4(p); }
 
+// x where d <= 0, else zero (whatever x is): a select would cost a compare and, at three times a
+// vector operation's rate, the select itself.
+__device__ __forceinline__ float kept(float x, int d) {
+  return __int_as_float(__float_as_int(x) & ((d - 1) >> 31));
+}
+
 template <int PASS>
 struct PassTraits {
   static constexpr bool kSum = PASS == kLinSumFwd || PASS == kLinSumRev;
@@ -239,8 +245,9 @@ constexpr size_t pass_lds_bytes() {
 struct PassShared {
   // the chunk's decays, by its parity: G (log2, hi + lo) and the factors of x's and y's rows
   __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
-  // dg's parts, by the chunk's parity; row and column sums of the pairs by the other side's half
-  float dots[2][4][64], rsum[2][2][64], csum[2][2][64];
+  // dg's parts, by the chunk's parity; the pairs' row sums (in the block on the diagonal, off it) and
+  // the columns' sums over each wave's tiles
+  float dots[2][4][64], rsum[2][2][64], csum[2][4][32];
   float s_decay[2];
   int unit[4];
 };
@@ -271,7 +278,8 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   E *const tp = PT::kDots ? tx : tx + 64 * LDX;
   auto &s_hi = sh.s_hi, &s_lo = sh.s_lo, &s_x = sh.s_x, &s_yf = sh.s_yf;
   auto &dots = sh.dots;
-  auto &rsum = sh.rsum, &csum = sh.csum;
+  auto &rsum = sh.rsum;
+  auto &csum = sh.csum;
   auto &s_decay = sh.s_decay;
   auto &sh_unit = sh.unit;
 
@@ -374,8 +382,14 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       }
     }
 
-  u32x4 sy[UPT], sz[UPT], sx[UPT], sw[UPT];  // the next chunk's rows
-  float sg = 0.f;                            // ... log decays (one wave)
+  // rows that are on their way, and their log decays (one wave): the next chunk's, in the sums the
+  // next two chunks' (their rounds are short against a load's latency)
+  constexpr int kSets = PT::kSum ? 2 : 1;
+  struct Rows {
+    u32x4 y[UPT], z[UPT], x[UPT], w[UPT];
+    float g;
+  };
+  Rows set[kSets];
   // Rows are read and written through buffer resources of the chunk's rows: the base is scalar, a
   // lane holds one 32-bit offset per row stride, and rows past the sequence's end are out of the
   // buffer's range, so they read as zeros and are not written.
@@ -398,19 +412,19 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       to[u] = __builtin_amdgcn_raw_buffer_load_b128(
           rsrc, at + kRows * u * heads * D * (int)sizeof(E), 0, 0);
   };
-  const auto fetch = [&](int ch) {
+  const auto fetch = [&](Rows &to, int ch) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
     const int n = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
-    load_rows(sy, py, t0, kYk, n);
-    load_rows(sz, pz, t0, kZk, n);
-    if (!PT::kSum) load_rows(sx, px, t0, kXk, n);
-    if (PT::kDots) load_rows(sw, pw, t0, true, n);
-    if (w == kDecayWave) sg = lane < n ? a.g[a.g_head ? h : (t0 + lane) * a.H + h] : 0.f;
+    load_rows(to.y, py, t0, kYk, n);
+    load_rows(to.z, pz, t0, kZk, n);
+    if (!PT::kSum) load_rows(to.x, px, t0, kXk, n);
+    if (PT::kDots) load_rows(to.w, pw, t0, true, n);
+    if (w == kDecayWave) to.g = lane < n ? a.g[a.g_head ? h : (t0 + lane) * a.H + h] : 0.f;
   };
   // the decays of the chunk that was fetched (one wave)
   F2 total{0.f, 0.f};  // the unit's whole log decay
-  const auto make_decays = [&](int par) {
-    const F2 G = wave_scan2(log2_decay(sg));
+  const auto make_decays = [&](float g, int par) {
+    const F2 G = wave_scan2(log2_decay(g));
     const F2 GC = F2{__shfl(G.hi, 63, 64), __shfl(G.lo, 63, 64)};
     const float from_start = exp2_fast(G.hi + G.lo);
     const float to_end = exp2_fast((GC.hi - G.hi) + (GC.lo - G.lo));
@@ -430,16 +444,23 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
     float *const to = PASS == kLinDq ? a.dg_q : a.dg_k;
     const float d = dots[par][0][lane] + dots[par][1][lane] + dots[par][2][lane] + dots[par][3][lane];
-    if (t < t_end) to[t * a.H + h] = d;
+    if (t < t_end) to[(int64_t)h * a.T + t] = d;
     if (PASS == kLinDq) {
-      // sum over the pairs s >= t > i = sum_{s >= t} (row sum - column sum); rows from the end
-      const float r1 = lane >= 32 ? rsum[par][1][lane] : 0.f, c0 = lane < 32 ? csum[par][0][lane] : 0.f;
-      const F2 x = add2(add2(F2{rsum[par][0][lane], 0.f}, F2{r1, 0.f}),
-                        add2(F2{-c0, 0.f}, F2{-csum[par][1][lane], 0.f}));
+      // sum over the pairs s >= t > i = sum_{s >= t} (row sum - column sum); rows from the end.  The
+      // first 32 rows have pairs in their own block only, the others' columns too.
+      F2 x = F2{rsum[par][0][lane], 0.f};
+      if (lane < 32) {
+        x = add2(x, F2{-csum[par][0][lane], 0.f});
+        x = add2(x, F2{-csum[par][1][lane], 0.f});
+        x = add2(x, F2{-csum[par][3][lane], 0.f});
+      } else {
+        x = add2(x, F2{rsum[par][1][lane], 0.f});
+        x = add2(x, F2{-csum[par][2][lane - 32], 0.f});
+      }
       const F2 up = wave_scan2(x);
       const float th = __shfl(up.hi, 63, 64), tl = __shfl(up.lo, 63, 64);
       const F2 rest = add2(add2(F2{th, tl}, F2{-up.hi, -up.lo}), x);
-      if (t < t_end) a.dg_pairs[t * a.H + h] = rest.hi + rest.lo;
+      if (t < t_end) a.dg_pairs[(int64_t)h * a.T + t] = rest.hi + rest.lo;
     }
   };
 
@@ -454,26 +475,28 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   // few chunks, which wait for memory and each other anyway, it would cost accuracy for nothing.
   const int state_terms = PT::kDots || nsteps <= kShortUnit ? kStateTerms : 1;
   if (nsteps > 0) {
-    fetch(ch);
-    if (w == kDecayWave) make_decays(0);
+    fetch(set[0], ch);
+    if (kSets > 1 && nsteps > 1) fetch(set[kSets - 1], ch + step);
+    if (w == kDecayWave) make_decays(set[0].g, 0);
   }
-  for (int it = 0; it < nsteps; ++it, ch += step) {
+  // one chunk, whose rows are in `in`; `next` holds the next chunk's
+  const auto round = [&](int it, Rows &in, Rows &next) {
     const int64_t t0 = t_beg + (int64_t)ch * kChunk;
     const int par = it & 1;
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
       const int row = r0 + kRows * u, oy = row * LDY + X::place(row, o0), ox = row * LDX + o0;
-      *reinterpret_cast<u32x4 *>(ty + oy) = sy[u];
-      *reinterpret_cast<u32x4 *>(tz + oy) = sz[u];
-      if (!PT::kSum) X::put_xw(tx + ox, sx[u]);
-      if (PT::kDots) X::put_xw(tw + ox, sw[u]);
+      *reinterpret_cast<u32x4 *>(ty + oy) = in.y[u];
+      *reinterpret_cast<u32x4 *>(tz + oy) = in.z[u];
+      if (!PT::kSum) X::put_xw(tx + ox, in.x[u]);
+      if (PT::kDots) X::put_xw(tw + ox, in.w[u]);
     }
     __syncthreads();
     const float *const g_hi = s_hi[par], *const g_lo = s_lo[par], *const f_x = s_x[par], *const f_y = s_yf[par];
     if (it > 0) flush_dots(ch - step, par ^ 1);
     // the next chunk's loads: at once, or (four tiles) once the first half's registers are free
-    if (!PT::kDots && it + 1 < nsteps) fetch(ch + step);
+    if (!PT::kDots && it + kSets < nsteps) fetch(in, ch + kSets * step);
 
     Frag zf[2][NT];  // z's columns of this wave: rows 32 kb + (order)
     const auto read_z = [&]() {
@@ -486,90 +509,110 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 
     f32x4 o[4][NT];  // the output by 16-row tiles
     if constexpr (!PT::kSum) {
-      // the pairs within the chunk: P by 32 x 32 blocks, three of them (the fourth is masked), one
-      // for each of waves 0 to 2
-      const int xb = PT::kRev ? w >> 1 : (w + 1) >> 1, yb = PT::kRev ? (w + 1) >> 1 : w >> 1;
-      f32x4 p[2][2];
-      if (w < 3) {
-        const E *const xrow = tx + (32 * xb + c) * LDX + 4 * gq, *const yrow = ty + (32 * yb + c) * LDY + row_y;
-        float xh[2], xl[2];
-        f32x4 yh[2], yl[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          xh[i] = g_hi[32 * xb + 16 * i + c], xl[i] = g_lo[32 * xb + 16 * i + c];
-          yh[i] = lds_f32x4(g_hi + 32 * yb + 16 * i + 4 * gq);
-          yl[i] = lds_f32x4(g_lo + 32 * yb + 16 * i + 4 * gq);
-          p[i][0] = p[i][1] = zero4();
-        }
-        const auto block = [&](const E *xr, const E *yr, f32x4(&acc)[2][2]) {
+      // the pairs within the chunk: P's ten 16 x 16 tiles, two or three per wave.  Waves 0 and 2: the
+      // 32 x 32 blocks on the diagonal (two tiles masked within, one whole, one that is zero); waves
+      // 1 and 3: 16 rows of x each of the block off it.
+      const bool diag = (w & 1) == 0;
+      const int xb = diag ? 16 * w : PT::kRev ? 16 * (w >> 1) : 32 + 16 * (w >> 1);  // first row of x
+      const int yb = diag ? 16 * w : PT::kRev ? 32 : 0;                             // ... of y
+      f32x4 p[3];  // on the diagonal: (0, 0), the whole one, (1, 1); off it: y's two tiles
+      float r_sum[2] = {0.f, 0.f};
+      const E *const xrow = tx + (xb + c) * LDX + 4 * gq, *const yrow = ty + (yb + c) * LDY + row_y;
+      const E *const wrow = tw + (xb + c) * LDX + 4 * gq, *const zrow = tz + (yb + c) * LDY + row_y;
+      const auto tiles = [&](const E *xr, const E *yr, f32x4(&acc)[3]) {
+        acc[0] = acc[1] = acc[2] = zero4();
+        if (diag) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            const Frag x0 = X::row(xr + 32 * ks), x1 = X::row(xr + 16 * LDX + 32 * ks);
-            const Frag y0 = X::row(yr + 32 * ks), y1 = X::row(yr + 16 * LDY + 32 * ks);
-            acc[0][0] = X::mma(y0, x0, acc[0][0]);
-            acc[0][1] = X::mma(y1, x0, acc[0][1]);
-            acc[1][0] = X::mma(y0, x1, acc[1][0]);
-            acc[1][1] = X::mma(y1, x1, acc[1][1]);
+            const Frag x_0 = X::row(xr + 32 * ks), x_1 = X::row(xr + 16 * LDX + 32 * ks);
+            const Frag y_0 = X::row(yr + 32 * ks), y_1 = X::row(yr + 16 * LDY + 32 * ks);
+            acc[0] = X::mma(y_0, x_0, acc[0]);
+            acc[1] = PT::kRev ? X::mma(y_1, x_0, acc[1]) : X::mma(y_0, x_1, acc[1]);
+            acc[2] = X::mma(y_1, x_1, acc[2]);
           }
-        };
-        block(xrow, yrow, p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = 32 * (yb - xb) + 16 * (k - i) + 4 * gq + j - c;  // y's token less x's
-              const bool in = PT::kRev ? d >= 0 : d <= 0;
-              const float e = PT::kRev ? (yh[k][j] - xh[i]) + (yl[k][j] - xl[i])
-                                       : (xh[i] - yh[k][j]) + (xl[i] - yl[k][j]);
-              const float v = s_p * (p[i][k][j] * exp2_fast(in ? e : 0.f));
-              p[i][k][j] = in ? v : 0.f;
-            }
-        if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed
-          f32x4 m[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) m[i][0] = m[i][1] = zero4();
-          sched_fence();
-          block(tw + (32 * xb + c) * LDX + 4 * gq, tz + (32 * yb + c) * LDY + row_y, m);
-          float r[2] = {0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float cs = 0.f;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const bool in = 32 * (yb - xb) + 16 * (k - i) + 4 * gq + j - c < 0;
-                const float x = in ? m[i][k][j] * p[i][k][j] : 0.f;
-                r[i] += x;
-                cs += x;
-              }
-              cs = row16_sum_dpp(cs);
-              if (c == 0) csum[par][xb][32 * yb + 16 * k + 4 * gq + j] = cs;
-            }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            r[i] += __shfl_xor(r[i], 16, 64);
-            r[i] += __shfl_xor(r[i], 32, 64);
-            if (gq == 0) rsum[par][yb][32 * xb + 16 * i + c] = r[i];
+          for (int ks = 0; ks < KS; ++ks) {
+            const Frag x_0 = X::row(xr + 32 * ks);
+            acc[0] = X::mma(X::row(yr + 32 * ks), x_0, acc[0]);
+            acc[1] = X::mma(X::row(yr + 16 * LDY + 32 * ks), x_0, acc[1]);
           }
         }
+      };
+      tiles(xrow, yrow, p);
+      // p of rows xo + c of x and yo + 4 gq .. of y, decayed; masked: only pairs in order
+      const auto decayed = [&](f32x4 v, int xo, int yo, bool masked) {
+        const float xh = g_hi[xo + c], xl = g_lo[xo + c];
+        const f32x4 yh = lds_f32x4(g_hi + yo + 4 * gq), yl = lds_f32x4(g_lo + yo + 4 * gq);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = PT::kRev ? (yh[j] - xh) + (yl[j] - xl) : (xh - yh[j]) + (xl - yl[j]);
+          v[j] = s_p * (v[j] * exp2_fast(e));
+          if (masked) v[j] = kept(v[j], PT::kRev ? c - (4 * gq + j) : 4 * gq + j - c);
+        }
+        return v;
+      };
+      if (diag) {
+        p[0] = decayed(p[0], xb, yb, true);
+        p[1] = decayed(p[1], PT::kRev ? xb : xb + 16, PT::kRev ? yb + 16 : yb, false);
+        p[2] = decayed(p[2], xb + 16, yb + 16, true);
+      } else {
+        p[0] = decayed(p[0], xb, yb, false);
+        p[1] = decayed(p[1], xb, yb + 16, false);
       }
+      if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed, by rows and columns
+        f32x4 m[3];
+        sched_fence();
+        tiles(wrow, zrow, m);
+        float cs[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float m0 = m[0][j] * p[0][j], m1 = m[1][j] * p[1][j];
+          if (diag) {
+            const int d = 4 * gq + j - c + 1;
+            const float a0 = kept(m0, d), a2 = kept(m[2][j] * p[2][j], d);
+            r_sum[0] += a0, r_sum[1] += m1 + a2;
+            cs[0][j] = a0 + m1, cs[1][j] = a2;
+          } else {
+            r_sum[0] += m0 + m1;
+            cs[0][j] = m0, cs[1][j] = m1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = row16_sum_dpp(cs[k][j]);
+            if (c == 0) csum[par][w][16 * k + 4 * gq + j] = x;
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          r_sum[i] += __shfl_xor(r_sum[i], 16, 64);
+          r_sum[i] += __shfl_xor(r_sum[i], 32, 64);
+        }
+        if (gq == 0) {
+          rsum[par][w & 1][xb + c] = r_sum[0];
+          if (diag) rsum[par][0][xb + 16 + c] = r_sum[1];
+        }
+      }
+      const auto store_tile = [&](int xt, int yt, f32x4 v) {
+        E *const to = tp + (p_slot<PT::kRev>(xt, yt) * kPTerms * 64 + lane) * 4;
+        store4(to, v);
+        if (kPTerms == 2) {
+          f32x4 unused = zero4();
+          X::residual(X::round(v, unused), v, unused);
+          store4(to + 256, v);
+        }
+      };
       const auto store_p = [&]() {
-        if (w < 3) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              E *const to = tp + (p_slot<PT::kRev>(2 * xb + i, 2 * yb + k) * kPTerms * 64 + lane) * 4;
-              store4(to, p[i][k]);
-              if (kPTerms == 2) {
-                f32x4 x = p[i][k], unused = zero4();
-                X::residual(X::round(x, unused), x, unused);
-                store4(to + 256, x);
-              }
-            }
+        const int xt = xb / 16, yt = yb / 16;
+        store_tile(xt, yt, p[0]);
+        if (diag) {
+          store_tile(PT::kRev ? xt : xt + 1, PT::kRev ? yt + 1 : yt, p[1]);
+          store_tile(xt + 1, yt + 1, p[2]);
+          store_tile(PT::kRev ? xt + 1 : xt, PT::kRev ? yt : yt + 1, zero4());
+        } else {
+          store_tile(xt, yt + 1, p[1]);
         }
       };
       if (!PT::kDots) store_p();
@@ -631,7 +674,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       lds_barrier();
       if (PT::kDots) {
         store_p();
-        if (it + 1 < nsteps) fetch(ch + step);
+        if (it + 1 < nsteps) fetch(in, ch + step);
         lds_barrier();
       }
 
@@ -730,7 +773,14 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
         sched_fence();
       }
     }
-    if (w == kDecayWave && it + 1 < nsteps) make_decays(par ^ 1);
+    if (w == kDecayWave && it + 1 < nsteps) make_decays(next.g, par ^ 1);
+  };
+  for (int it = 0; it < nsteps; it += kSets, ch += step) {
+    round(it, set[0], set[kSets - 1]);
+    if (kSets > 1 && it + 1 < nsteps) {
+      ch += step;
+      round(it + 1, set[kSets - 1], set[0]);
+    }
   }
   if (PT::kDots && nsteps > 0) {
     __syncthreads();
@@ -811,61 +861,58 @@ namespace {
 
 // The states at the units' starts from the units' own sums, in place: along each sequence of more
 // than one unit, S <- decay_u S + sum_u, written where unit u + 1's sum was.  rev: the gradients at
-// the units' ends, from the last unit to the first.  One thread per two elements of a state, its
-// loads kAhead units ahead of the chain: a chain's step is two instructions, so the time is that of
-// the bytes in flight (32K tokens x 8 heads, 57 units: 33 us with 4 units of 16 bytes ahead).
-constexpr int kAhead = 16;
-typedef float f32x2 __attribute__((ext_vector_type(2)));
+// the units' ends, from the last unit to the first.  One thread per four elements of a state, its
+// loads kAhead units ahead of the chain: a chain's step is a few instructions, so the time is that
+// of the bytes in flight.
+constexpr int kAhead = 16, kScanThreads = 128;
 
 template <bool REV>
 __device__ __forceinline__ void lin_scan(const LinArgs &a, int D, int64_t e) {
-  const int seq = blockIdx.x, h = blockIdx.y;
+  const int seq = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
   const int64_t DD = (int64_t)D * D;
-  const int32_t b0 = a.cu[seq], b1 = a.cu[seq + 1];
-  if (b0 < 0 || b1 < b0 || b1 > a.T || e >= DD) return;
+  const int32_t b0 = __builtin_amdgcn_readfirstlane(a.cu[seq]), b1 = __builtin_amdgcn_readfirstlane(a.cu[seq + 1]);
+  if (b0 < 0 || b1 < b0 || b1 > a.T) return;
   const int nch = (b1 - b0 + kChunk - 1) / kChunk, nu = (nch + a.L - 1) / a.L;
   if (nu < 2) return;
-  const int64_t u0 = a.seq_unit[seq];
+  const int64_t u0 = __builtin_amdgcn_readfirstlane(a.seq_unit[seq]);
   if (u0 < 0 || u0 + nu > a.units) return;  // a malformed table gave this sequence no units
   const int64_t row = (int64_t)a.H * DD;
   float *const st = (REV ? a.unit_r : a.unit_s) + u0 * row + h * DD + e;
   const float *const dec = a.unit_decay + (REV ? a.units * a.H : 0) + u0 * a.H + h;
-  f32x2 S = {0.f, 0.f};
+  f32x4 S = zero4();
   const float *init = REV ? (a.dht ? a.dht + ((int64_t)seq * a.H + h) * DD + e : nullptr)
                           : (a.h0 ? a.h0 + seq * a.h0_stride + h * DD + e : nullptr);
-  if (init) S = *reinterpret_cast<const f32x2 *>(init);
+  if (init) S = *reinterpret_cast<const f32x4 *>(init);
   // step s passes unit us(s) and writes the state to unit us(s + 1), whose sum was read kAhead
   // steps before its own step, so always before that write
   const int steps = nu - 1;
   const auto us = [&](int s) { return REV ? nu - 1 - s : s; };
-  f32x2 b[kAhead];
-  float d[kAhead];
+  f32x4 b[kAhead];
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) {
-    const int s = min(j, steps - 1);
-    b[j] = *reinterpret_cast<const f32x2 *>(st + us(s) * row);
-    d[j] = dec[(int64_t)us(s) * a.H];
-  }
-  for (int s0 = 0; s0 < steps; s0 += kAhead) {
+  for (int j = 0; j < kAhead; ++j)
+    if (j < steps) b[j] = *reinterpret_cast<const f32x4 *>(st + us(j) * row);
+  for (int s64 = 0; s64 < steps; s64 += 64) {  // 64 units' decays, one in each lane
+    const float dl = s64 + lane < steps ? dec[(int64_t)us(s64 + lane) * a.H] : 0.f;
+    const int end = min(steps, s64 + 64);
+    for (int s0 = s64; s0 < end; s0 += kAhead) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int s = s0 + j;
-      if (s < steps) {
-        S = d[j] * S + b[j];
-        if (s + kAhead < steps) {
-          b[j] = *reinterpret_cast<const f32x2 *>(st + us(s + kAhead) * row);
-          d[j] = dec[(int64_t)us(s + kAhead) * a.H];
+      for (int j = 0; j < kAhead; ++j) {
+        const int s = s0 + j;
+        if (s < end) {
+          const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(dl), s & 63));
+          S = d * S + b[j];
+          if (s + kAhead < steps) b[j] = *reinterpret_cast<const f32x4 *>(st + us(s + kAhead) * row);
+          *reinterpret_cast<f32x4 *>(st + us(s + 1) * row) = S;
         }
-        *reinterpret_cast<f32x2 *>(st + us(s + 1) * row) = S;
       }
     }
   }
 }
 
 // grid z: D^2 / 512 pieces of the states, then (both directions) as many of the state gradients
-__global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
-  const int pieces = D * D / 512, z = blockIdx.z;
-  const int64_t e = ((int64_t)(z < pieces ? z : z - pieces) * 256 + threadIdx.x) * 2;
+__global__ __launch_bounds__(kScanThreads) void lin_scan_kernel(LinArgs a, int D) {
+  const int pieces = D * D / (4 * kScanThreads), z = blockIdx.z;
+  const int64_t e = ((int64_t)(z < pieces ? z : z - pieces) * kScanThreads + threadIdx.x) * 4;
   if (z < pieces) lin_scan<false>(a, D, e);
   else lin_scan<true>(a, D, e);
 }
@@ -877,8 +924,18 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(LinArgs a, int D) {
 // unit's end.  One workgroup per (unit, head), from the unit's end by blocks of 64 chunks: the waves
 // sum their chunks side by side, then finish them with the sums of the later ones.  A token whose
 // decay is zero in fp32 has no gradient.
+__device__ __forceinline__ F2 lane_of(F2 x, int l) {
+  return F2{__shfl(x.hi, l, 64), __shfl(x.lo, l, 64)};
+}
+// ... of a lane that is the same for the whole wave (and may be inactive)
+__device__ __forceinline__ F2 lane_of_uniform(F2 x, int l) {
+  return F2{__int_as_float(__builtin_amdgcn_readlane(__float_as_int(x.hi), l)),
+            __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x.lo), l))};
+}
+
 __global__ __launch_bounds__(256) void lin_dg_kernel(LinArgs a) {
-  __shared__ double sums[64], part[4];
+  __shared__ F2 sums[64];
+  __shared__ double part[4];
   __shared__ int sh_unit[3];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, h = blockIdx.y;
   const int64_t uh = (int64_t)blockIdx.x * a.H + h;
@@ -897,49 +954,45 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(LinArgs a) {
   const bool ok = seq >= 0 && t_beg >= 0 && t_end >= t_beg && t_end <= a.T && c1 > c0;
   double total = 0.0;
   if (ok) {
-    double b = (double)a.unit_dot[uh];
+    const float *const dq = a.dg_q + (int64_t)h * a.T, *const dk = a.dg_k + (int64_t)h * a.T;
+    const float *const pairs = a.dg_pairs + (int64_t)h * a.T;
+    F2 b = F2{a.unit_dot[uh], 0.f};  // <S, dS> at the end of the block
     const float gh = a.g_head ? a.g[h] : 0.f;
+    // x and the later lanes' x: the wave's sum less the sum before
+    const auto from_here = [&](F2 x, F2 &all) {
+      const F2 up = wave_scan2(x);
+      all = lane_of(up, 63);
+      return add2(add2(all, F2{-up.hi, -up.lo}), x);
+    };
     for (int hi = c1; hi > c0; hi -= 64) {  // chunks [lo, hi)
       const int lo = max(c0, hi - 64), n = hi - lo;
 #pragma unroll 4
       for (int j = w; j < n; j += 4) {
-        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane, i = t * a.H + h;
-        const double s = wave_sum_f64(t < t_end ? (double)a.dg_q[i] - (double)a.dg_k[i] : 0.0);
-        if (lane == 0) sums[j] = s;
+        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane;
+        F2 all;
+        from_here(t < t_end ? add2(F2{dq[t], 0.f}, F2{-dk[t], 0.f}) : F2{0.f, 0.f}, all);
+        if (lane == 0) sums[j] = all;
       }
       __syncthreads();
-      // the sums of the chunks after each one, within the block
-      double after = 0.0, all = 0.0;
-      {
-        const double x = lane < n ? sums[lane] : 0.0;
-        double s = x;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const double y = __shfl_down(s, off, 64);
-          if (lane + off < 64) s += y;
-        }
-        after = s - x;
-        all = __shfl(s, 0, 64);
-      }
+      // lane j: the sum of the block's chunks after chunk j
+      const F2 x = lane < n ? sums[lane] : F2{0.f, 0.f};
+      F2 whole;
+      const F2 after = add2(from_here(x, whole), F2{-x.hi, -x.lo});
 #pragma unroll 2
       for (int j = w; j < n; j += 4) {
-        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane, i = t * a.H + h;
+        const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane;
         const bool in = t < t_end;
-        double s = in ? (double)a.dg_q[i] - (double)a.dg_k[i] : 0.0;  // from this lane on
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const double y = __shfl_down(s, off, 64);
-          if (lane + off < 64) s += y;
-        }
-        const double from_end = b + __shfl(after, j, 64);
+        F2 all;
+        const F2 s = from_here(in ? add2(F2{dq[t], 0.f}, F2{-dk[t], 0.f}) : F2{0.f, 0.f}, all);
         if (in) {
-          const F2 lg = log2_decay(a.g_head ? gh : a.g[i]);
-          const double dg = lg.hi <= kNoDecay ? 0.0 : (double)a.dg_pairs[i] + s + from_end;
-          if (!a.g_head) a.dg[i] = (float)dg;
-          total += dg;
+          const F2 lg = log2_decay(a.g_head ? gh : a.g[t * a.H + h]);
+          F2 dg = add2(add2(add2(b, lane_of_uniform(after, j)), s), F2{pairs[t], 0.f});
+          if (lg.hi <= kNoDecay) dg = F2{0.f, 0.f};
+          if (!a.g_head) a.dg[t * a.H + h] = dg.hi + dg.lo;
+          total += (double)dg.hi + (double)dg.lo;
         }
       }
-      b += all;
+      b = add2(b, whole);
       __syncthreads();
     }
   }
@@ -1002,7 +1055,8 @@ hipError_t launch_stage_of(const LinArgs &a, int D, bool is_bf16, hipStream_t st
 }
 
 hipError_t launch_scan(const LinArgs &a, int D, int directions, hipStream_t stream) {
-  hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)a.N, a.H, directions * (D * D / 512)), dim3(256), 0,
+  hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)a.N, a.H, directions * (D * D / (4 * kScanThreads))),
+                     dim3(kScanThreads), 0,
                      stream, a, D);
   return hipGetLastError();
 }
