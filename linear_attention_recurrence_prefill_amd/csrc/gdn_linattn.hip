@@ -28,6 +28,7 @@
 // are exponentiated, so no factor overflows and far tokens keep their precision.  Log decays below
 // kMinLog2 have no fp32 value above zero and are taken as kMinLog2: -inf empties the state.
 #include <algorithm>
+#include <atomic>
 
 #include "gdn_device.h"
 #include "gdn_internal.h"
@@ -340,12 +341,8 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 
   // this wave's columns of the state: tile t's column of lane c, and the first column that the
   // lane addresses in a transposing read; in an output tile the lane has columns out_col + 4 t ..
-  int col[NT], z_at[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    col[t] = NT == 2 ? 32 * w + 8 * (c >> 2) + 4 * t + (c & 3) : 16 * w + c;
-    z_at[t] = X::column_base(NT == 2 ? 32 * w + 8 * (c & 3) + 4 * t : 16 * w + 4 * (c & 3), col[t], c, gq, LDY);
-  }
+  const int col = NT == 2 ? 32 * w + 8 * (c >> 2) + (c & 3) : 16 * w + c;  // (tile 1: 4 further)
+  const int z_at = X::column_base(NT == 2 ? 32 * w + 8 * (c & 3) : 16 * w + 4 * (c & 3), col, c, gq, LDY);
   const int y_at = X::column_base(4 * (c & 3), c, c, gq, LDY);
   const int out_col = NT == 2 ? 32 * w + 8 * gq : 16 * w + 4 * gq;
   const int row_y = X::place(c, 4 * gq);    // a row operand's first element in y or z (rows 16 i + c)
@@ -355,7 +352,6 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   const bool f32_out = PT::kDots && a.grad_f32;   // dq, dk of grouped heads: fp32 per value head
   const bool per_k = PT::kDots && !f32_out;
   const int out_heads = per_k ? a.HK : a.H, out_head = per_k ? hk : h;
-  const int v_out = c * out_heads * D + out_col;
 
   f32x4 S[MT][NT];
   const float *src = nullptr;
@@ -374,10 +370,10 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       if (src) {
         const int r = 16 * m + 4 * gq;
         if (PT::kTransposed) {
-          S[m][t] = *reinterpret_cast<const f32x4 *>(src + col[t] * D + r);
+          S[m][t] = *reinterpret_cast<const f32x4 *>(src + (col + 4 * t) * D + r);
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) S[m][t][j] = src[(r + j) * D + col[t]];
+          for (int j = 0; j < 4; ++j) S[m][t][j] = src[(r + j) * D + col + 4 * t];
         }
       }
     }
@@ -400,13 +396,12 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0,
                                              ((n - 1) * heads + 1) * D * size, 0x00020000);
   };
-  // the lane's offset in the first round's rows, per row stride
-  const int vh = (r0 * a.H * D + o0) * (int)sizeof(E), vk = (r0 * a.HK * D + o0) * (int)sizeof(E);
   const auto load_rows = [&](u32x4(&to)[UPT], const void *base, int64_t t0, bool of_k, int n) {
     const int heads = of_k ? a.HK : a.H;
     const auto rsrc = rows_of(base, t0, heads, of_k ? hk : h, n, sizeof(E));
-    int at = of_k ? vk : vh;
-    asm("" : "+v"(at));  // the rounds' offsets are made here, not kept
+    int mine = tid;
+    asm("" : "+v"(mine));  // the lane's offset in the first round's rows: made here, not kept
+    const int at = (mine / UPR * heads * D + mine % UPR * EPU) * (int)sizeof(E);
 #pragma unroll
     for (int u = 0; u < UPT; ++u)
       to[u] = __builtin_amdgcn_raw_buffer_load_b128(
@@ -503,7 +498,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) zf[kb][t] = X::template column<LDY>(tz + 32 * kb * LDY, z_at[t]);
+        for (int t = 0; t < NT; ++t) zf[kb][t] = X::template column<LDY>(tz + 32 * kb * LDY + 4 * t, z_at);
     };
     if constexpr (PT::kSum) read_z();
 
@@ -717,8 +712,9 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     if constexpr (!PT::kSum) {
       const int n_rows = (int)(t_end - t0 < kChunk ? t_end - t0 : kChunk);
       const auto rsrc = rows_of(out, t0, out_heads, out_head, n_rows, f32_out ? 4 : (int)sizeof(E));
-      int v_row = v_out;
-      asm("" : "+v"(v_row));
+      int c_row = c;
+      asm("" : "+v"(c_row));
+      const int v_row = c_row * out_heads * D + out_col;
 #pragma unroll
       for (int xt = 0; xt < 4; ++xt) {
         const int at = v_row + 16 * xt * out_heads * D;
@@ -787,13 +783,17 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     flush_dots(ch - step, (nsteps - 1) & 1);
   }
 
+  // the same column, made anew: not a register through all rounds
+  int c_end = lane & 15;
+  asm("" : "+v"(c_end));
+  const int col_end = NT == 2 ? 32 * w + 8 * (c_end >> 2) + (c_end & 3) : 16 * w + c_end;
   const auto store_state = [&](float *to) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[(16 * m + 4 * gq + j) * D + col[t]] = S[m][t][j];
+        for (int j = 0; j < 4; ++j) to[(16 * m + 4 * gq + j) * D + col_end + 4 * t] = S[m][t][j];
   };
   if (PT::kSum) {
     store_state((PT::kRev ? a.unit_r : a.unit_s) + uh * D * D);
@@ -811,7 +811,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const f32x4 x = *reinterpret_cast<const f32x4 *>(ds + col[t] * D + 16 * m + 4 * gq);
+          const f32x4 x = *reinterpret_cast<const f32x4 *>(ds + (col_end + 4 * t) * D + 16 * m + 4 * gq);
           float s = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) s += x[j] * S[m][t][j];
@@ -1036,10 +1036,18 @@ template <class E, int D, int WHAT>
 hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
   constexpr size_t lds = stage_lds_bytes<E, D, WHAT>();
   constexpr int kinds = WHAT == kGroupSums ? 2 : WHAT == kGroupGrads ? 3 : 1;
-  const void *kernel = reinterpret_cast<const void *>(&lin_stage_kernel<E, D, WHAT>);
-  if (lds > 65536) {  // above the default limit of dynamic LDS
-    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (lds > 65536) {  // above the default limit of dynamic LDS, which is raised once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_stage_kernel<E, D, WHAT>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+      if (dev <= 63) raised.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   const unsigned u = (unsigned)a.units, h = (unsigned)a.H;
   hipLaunchKernelGGL((lin_stage_kernel<E, D, WHAT>),

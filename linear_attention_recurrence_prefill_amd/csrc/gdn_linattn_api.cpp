@@ -48,24 +48,33 @@ int32_t k_heads(const gdn_linattn_problem *p) {
   return p->num_k_heads > 0 ? p->num_k_heads : p->num_heads;
 }
 
-// Length in chunks of the units that sequences are split into (0: one unit per sequence).  Enough
-// units that every slot has one; a unit is at least kMinSegment chunks, since splitting costs a
-// second read of k and v and each unit's state, written and read.
-constexpr int32_t kMinSegment = 4;
+// Length in chunks of the units that sequences are split into (0: one unit per sequence).  A unit's
+// chunks are a chain, run twice; each unit costs its state, written, joined and read.  The sum is
+// least at a length proportional to sqrt(chunks x heads / slots), the latency model of "How to Speed
+// Up GDN Kernels for Qwen Models", section "Lever 1"; the factors are fitted to sweeps of the length
+// (bf16, d = 128: best at 1, 2, 5, 8, 16 chunks for 64, 256, 1024, 4096, 8192 chunks x heads; within
+// a tenth of the best there).  fp32's products are sixteen times dearer, so its chains are cut
+// shorter.  Sequences that fill the slots by themselves, or are no longer than a unit, stay whole.
 gdn_status segment_chunks(const gdn_linattn_problem *p, int32_t *L) {
   *L = p->seg_chunks;
-  const int64_t nc = ceil_div(p->total_tokens, gdn::kChunk) + p->num_seqs;
-  if (*L == 0) {
-    int slots = p->num_slots;
-    if (slots == 0) {
-      gdn_status s = device_info(&slots);
-      if (s != GDN_OK) return s;
-      slots *= gdn::linattn_blocks_per_cu(p->head_dim, p->dtype == GDN_DTYPE_BF16);
-    }
-    const int64_t want = std::max<int64_t>(kMinSegment, ceil_div(nc * p->num_heads, slots));
-    if (nc > 2 * want && (int64_t)p->num_seqs * p->num_heads < 2 * slots)
-      *L = (int32_t)std::min<int64_t>(want, INT32_MAX);
+  if (*L > 0) return GDN_OK;
+  int slots = p->num_slots;
+  if (slots == 0) {
+    gdn_status s = device_info(&slots);
+    if (s != GDN_OK) return s;
+    slots *= gdn::linattn_blocks_per_cu(p->head_dim, p->dtype == GDN_DTYPE_BF16);
   }
+  const int64_t nc = ceil_div(p->total_tokens, gdn::kChunk);
+  const double factor = p->dtype == GDN_DTYPE_BF16 ? 3.5 : 1.8;
+  const double want = std::max(1.0, std::round(factor * std::sqrt((double)nc * p->num_heads / slots)));
+  if ((int64_t)p->num_seqs * p->num_heads >= 2 * (int64_t)slots || nc <= want * p->num_seqs) return GDN_OK;
+  // Units that nearly fill the slots a whole number of times are made to do so: the last of a
+  // sequence is on average half a unit.
+  const double partial = 0.5 * p->num_seqs;
+  const double rounds = std::round((nc / want + partial) * p->num_heads / slots);
+  const double units = rounds * slots / p->num_heads - partial;
+  const double fit = units >= 1.0 ? std::ceil(nc / units) : want;
+  *L = (int32_t)std::min<double>(fit, INT32_MAX);
   return GDN_OK;
 }
 

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from .gdn import (GDN_DTYPE_BF16, GDN_DTYPE_F32, _check, _check_out, _nbytes, _ptr, _workspace,
+from .gdn import (GDN_DTYPE_BF16, GDN_DTYPE_F32, _check, _check_out, _nbytes, _workspace,
                   load_library)
 
 
@@ -43,14 +43,31 @@ def _on(device):
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None:  # the same handle without a stream object
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _same_device(ref, **tensors):
+def _at(t):
+    """A tensor's address as the C calls take it (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(device, **tensors):
+    index = device.index
     for name, t in tensors.items():
-        if t is not None and (t.device != ref.device or not t.is_cuda or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous device tensor on {ref.device}")
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous device tensor on {device}")
+
+
+def _device_of(t):
+    if not t.is_cuda:
+        raise ValueError("inputs must be contiguous device tensors")
+    return t.device
 
 
 def _no_overlap(name, out, *inputs):
@@ -74,9 +91,9 @@ def _heads(q, k, v, g, rows):
         raise ValueError(f"q, k and v must be [{rows}, heads, D]")
     n, Hk, D = q.shape
     H = v.shape[1]
-    if tuple(k.shape) != (n, Hk, D) or tuple(v.shape) != (n, H, D) or Hk < 1 or H % Hk != 0:
+    if k.shape != (n, Hk, D) or v.shape != (n, H, D) or Hk < 1 or H % Hk != 0:
         raise ValueError(f"q and k must be [{rows}, Hk, D] and v [{rows}, H, D] with Hk dividing H")
-    if tuple(g.shape) not in ((n, H), (H,)):
+    if g.shape != (n, H) and g.shape != (H,):
         raise ValueError(f"g must be [{rows}, H], or [H] for a constant decay per head")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("k and v must have q's dtype")
@@ -89,10 +106,8 @@ def _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots):
     T, H, Hk, D, head = _heads(q, k, v, g, "T")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor of at least two offsets")
-    dtype = _dtype_of(q)
-    if not q.is_cuda:
-        raise ValueError("inputs must be contiguous device tensors")
-    _same_device(q, q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, h0=h0)
+    dtype, device = _dtype_of(q), _device_of(q)
+    _same_device(device, q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, h0=h0)
     N = cu_seqlens.numel() - 1
     stride = H * D * D
     if h0 is not None:
@@ -104,7 +119,7 @@ def _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots):
             raise ValueError("h0 must be [N, H, D, D] or [H, D, D] (shared by all sequences)")
     p = LinattnProblem(T, N, H, Hk, D, dtype, head, int(seg_chunks), int(num_slots), float(scale), 0,
                        stride)
-    return p, T, N, H, D
+    return p, device, N, H, D
 
 
 def _workspace_bytes(fn, p):
@@ -118,26 +133,26 @@ def linattn_fwd(q, k, v, g, cu_seqlens, h0=None, *, scale=1.0, seg_chunks=0, num
     """Forward: q, k [T, Hk, D], v [T, H, D] (bf16 or fp32; value head h reads key head
     h // (H // Hk)), g fp32 log decays [T, H] or [H], cu_seqlens int32 [N + 1], h0 fp32
     [N, H, D, D] or [H, D, D] (shared by all sequences).  Returns (o, final states or None)."""
-    p, T, N, H, D = _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots)
+    p, device, N, H, D = _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots)
     ins = (q, k, v, g, cu_seqlens, h0)
     if out is not None:
-        _check_out("out", out, tuple(v.shape), v.dtype, q.device)
+        _check_out("out", out, tuple(v.shape), v.dtype, device)
         _no_overlap("out", out, *ins)
     if final_state is not None:
-        _check_out("final_state", final_state, (N, H, D, D), torch.float32, q.device)
+        _check_out("final_state", final_state, (N, H, D, D), torch.float32, device)
         _no_overlap("final_state", final_state, *ins)
     lib = load_library()
-    with _on(q.device):
+    with _on(device):
         nbytes = _workspace_bytes(lib.gdn_linattn_fwd_workspace_size, p)
-        ws = _workspace(workspace, nbytes, q.device) if nbytes or workspace is not None else None
+        ws = _workspace(workspace, nbytes, device) if nbytes or workspace is not None else None
         o = out if out is not None else torch.empty_like(v)
         ht = None
         if output_final_state:
             ht = final_state if final_state is not None else torch.empty(
-                (N, H, D, D), dtype=torch.float32, device=q.device)
-        _check(lib.gdn_linattn_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                   _ptr(cu_seqlens), _ptr(h0), _ptr(o), _ptr(ht), _ptr(ws),
-                                   0 if ws is None else _nbytes(ws), _stream_of(q.device)))
+                (N, H, D, D), dtype=torch.float32, device=device)
+        _check(lib.gdn_linattn_fwd(ctypes.byref(p), _at(q), _at(k), _at(v), _at(g),
+                                   _at(cu_seqlens), _at(h0), _at(o), _at(ht), _at(ws),
+                                   0 if ws is None else _nbytes(ws), _stream_of(device)))
     return o, ht
 
 
@@ -147,25 +162,24 @@ def linattn_bwd(q, k, v, g, cu_seqlens, dout, h0=None, dht=None, *, scale=1.0, n
     states' gradient dht fp32 [N, H, D, D].  Returns dict(dq, dk, dv, dg, dh0): dq, dk summed over
     the value heads that share a key head, dg fp32 in g's shape, dh0 fp32 [N, H, D, D], or [H, D, D]
     summed over the sequences when h0 is shared (None without need_dh0)."""
-    p, T, N, H, D = _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots)
+    p, device, N, H, D = _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots)
     if tuple(dout.shape) != tuple(v.shape) or dout.dtype != q.dtype:
         raise ValueError("dout must have v's shape and q's dtype")
     if dht is not None and (tuple(dht.shape) != (N, H, D, D) or dht.dtype != torch.float32):
         raise ValueError("dht must be float32 [N, H, D, D]")
-    _same_device(q, dout=dout, dht=dht)
+    _same_device(device, dout=dout, dht=dht)
     lib = load_library()
-    with _on(q.device):
-        ws = _workspace(workspace, _workspace_bytes(lib.gdn_linattn_bwd_workspace_size, p), q.device)
+    with _on(device):
+        ws = _workspace(workspace, _workspace_bytes(lib.gdn_linattn_bwd_workspace_size, p), device)
         res = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                    dg=torch.empty_like(g), dh0=None)
         if need_dh0:
             res["dh0"] = torch.empty((H, D, D) if p.h0_seq_stride == 0 else (N, H, D, D),
-                                     dtype=torch.float32, device=q.device)
-        _check(lib.gdn_linattn_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                   _ptr(cu_seqlens), _ptr(h0), _ptr(dout), _ptr(dht),
-                                   _ptr(res["dq"]), _ptr(res["dk"]), _ptr(res["dv"]),
-                                   _ptr(res["dg"]), _ptr(res["dh0"]), _ptr(ws), _nbytes(ws),
-                                   _stream_of(q.device)))
+                                     dtype=torch.float32, device=device)
+        _check(lib.gdn_linattn_bwd(ctypes.byref(p), _at(q), _at(k), _at(v), _at(g), _at(cu_seqlens),
+                                   _at(h0), _at(dout), _at(dht), _at(res["dq"]), _at(res["dk"]),
+                                   _at(res["dv"]), _at(res["dg"]), _at(res["dh0"]), _at(ws),
+                                   _nbytes(ws), _stream_of(device)))
     return res
 
 
@@ -176,23 +190,22 @@ def linattn_step(q, k, v, g, state, pages=None, *, scale=1.0, out=None):
     output is zero).  Returns o [B, H, D]."""
     B, H, Hk, D, head = _heads(q, k, v, g, "B")
     dtype = _dtype_of(q)
-    if state.dtype != torch.float32 or state.dim() != 4 or tuple(state.shape[1:]) != (H, D, D) or \
+    if state.dtype != torch.float32 or state.dim() != 4 or state.shape[1:] != (H, D, D) or \
             (pages is None and state.shape[0] != B):
         raise ValueError("state must be float32 [B, H, D, D], or a pool [P, H, D, D] with pages")
-    if pages is not None and (pages.dtype != torch.int32 or tuple(pages.shape) != (B,)):
+    if pages is not None and (pages.dtype != torch.int32 or pages.shape != (B,)):
         raise ValueError("pages must be int32 [B]")
-    if not q.is_cuda:
-        raise ValueError("inputs must be contiguous device tensors")
-    _same_device(q, q=q, k=k, v=v, g=g, state=state, pages=pages)
+    device = _device_of(q)
+    _same_device(device, q=q, k=k, v=v, g=g, state=state, pages=pages)
     if out is not None:
-        _check_out("out", out, tuple(v.shape), v.dtype, q.device)
+        _check_out("out", out, tuple(v.shape), v.dtype, device)
         _no_overlap("out", out, q, k, v, g, state, pages)
     lib = load_library()
-    with _on(q.device):
+    with _on(device):
         o = out if out is not None else torch.empty_like(v)
-        _check(lib.gdn_linattn_step(B, H, Hk, D, dtype, head, float(scale), _ptr(q), _ptr(k),
-                                    _ptr(v), _ptr(g), _ptr(pages), state.shape[0], _ptr(state),
-                                    _ptr(o), _stream_of(q.device)))
+        _check(lib.gdn_linattn_step(B, H, Hk, D, dtype, head, scale, _at(q), _at(k), _at(v), _at(g),
+                                    _at(pages), state.shape[0], _at(state), _at(o),
+                                    _stream_of(device)))
     return o
 
 

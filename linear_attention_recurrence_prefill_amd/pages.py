@@ -8,11 +8,12 @@ sets a fault flag (``device_faults()``: ``FAULT_PAGE_*``) and its entry is left 
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from .gdn import _check, _nbytes, _ptr, _workspace, load_library
-from .linattn import _on, _same_device, _stream_of
+from .gdn import _check, _nbytes, _workspace, load_library
+from .linattn import _at, _on, _same_device, _stream_of
 
 # Bits of device_faults() that page numbers can set.
 FAULT_PAGE_RANGE, FAULT_PAGE_TWICE, FAULT_NO_PAGE = 2, 4, 8
@@ -33,6 +34,7 @@ def _index(name, x, shape=None):
                          (f" of {shape[0]} entries" if shape is not None else ""))
 
 
+@functools.lru_cache(maxsize=256)
 def pages_workspace_bytes(num_pages, count):
     """Workspace bytes of the calls below (gdn_pages_workspace_size)."""
     n = ctypes.c_size_t(0)
@@ -51,13 +53,13 @@ def pages_copy(dst, src, dst_pages, src_pages, *, workspace=None):
         raise ValueError("dst and src must have pages of the same type and size")
     _index("dst_pages", dst_pages)
     _index("src_pages", src_pages, tuple(dst_pages.shape))
-    _same_device(dst, src=src, dst_pages=dst_pages, src_pages=src_pages)
+    _same_device(dst.device, src=src, dst_pages=dst_pages, src_pages=src_pages)
     lib = load_library()
     n = dst_pages.numel()
     with _on(dst.device):
         ws = _workspace(workspace, pages_workspace_bytes(0, n), dst.device)
-        _check(lib.gdn_pages_copy(_ptr(dst), P, _ptr(src), Ps, nbytes, _ptr(dst_pages),
-                                  _ptr(src_pages), n, _ptr(ws), _nbytes(ws),
+        _check(lib.gdn_pages_copy(_at(dst), P, _at(src), Ps, nbytes, _at(dst_pages),
+                                  _at(src_pages), n, _at(ws), _nbytes(ws),
                                   _stream_of(dst.device)))
     return dst
 
@@ -71,15 +73,15 @@ def pages_fork(pool, live, parents, *, children=None, workspace=None):
     _index("parents", parents)
     if children is not None:
         _index("children", children, tuple(parents.shape))
-        if children.data_ptr() == parents.data_ptr() and parents.numel():
+        if children.data_at() == parents.data_at() and parents.numel():
             raise ValueError("children must not overlap parents")
-    _same_device(pool, live=live, parents=parents, children=children)
+    _same_device(pool.device, live=live, parents=parents, children=children)
     lib = load_library()
     with _on(pool.device):
         res = children if children is not None else torch.empty_like(parents)
         ws = _workspace(workspace, pages_workspace_bytes(P, 0), pool.device)
-        _check(lib.gdn_pages_fork(_ptr(pool), _ptr(live), P, nbytes, _ptr(parents), parents.numel(),
-                                  _ptr(res), _ptr(ws), _nbytes(ws), _stream_of(pool.device)))
+        _check(lib.gdn_pages_fork(_at(pool), _at(live), P, nbytes, _at(parents), parents.numel(),
+                                  _at(res), _at(ws), _nbytes(ws), _stream_of(pool.device)))
     return res
 
 
@@ -89,10 +91,10 @@ def pages_free(live, pages):
         raise ValueError("live must be a contiguous device tensor")
     _index("live", live)
     _index("pages", pages)
-    _same_device(live, live=live, pages=pages)
+    _same_device(live.device, live=live, pages=pages)
     lib = load_library()
     with _on(live.device):
-        _check(lib.gdn_pages_free(_ptr(live), live.numel(), _ptr(pages), pages.numel(),
+        _check(lib.gdn_pages_free(_at(live), live.numel(), _at(pages), pages.numel(),
                                   _stream_of(live.device)))
 
 
@@ -101,12 +103,12 @@ def pages_compact(pool, live, *, workspace=None):
     [P]: where each page went, -1 for a free one."""
     P, nbytes = _pool("pool", pool)
     _index("live", live, (P,))
-    _same_device(pool, live=live)
+    _same_device(pool.device, live=live)
     lib = load_library()
     with _on(pool.device):
         remap = torch.empty_like(live)
         ws = _workspace(workspace, pages_workspace_bytes(P, 0), pool.device)
-        _check(lib.gdn_pages_compact(_ptr(pool), _ptr(live), P, nbytes, _ptr(remap), _ptr(ws),
+        _check(lib.gdn_pages_compact(_at(pool), _at(live), P, nbytes, _at(remap), _at(ws),
                                      _nbytes(ws), _stream_of(pool.device)))
     return remap
 

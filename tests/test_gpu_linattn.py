@@ -2,8 +2,10 @@
 (tests/linattn_ref.py, gradients by autograd; gfx950 only; marked ``gpu``).
 
 Tolerances, as relative L2 over a tensor.  bf16 outputs carry one rounding of at most 2^-8 of each
-value; everything before it is held to 2^-16 (operands split into two bf16 terms) or better, so
-2^-8 + 2^-12 bounds the distance.  fp32 results are sums: each addition or product rounds by at most
+value, rho = 2^-8 / sqrt 3 in the mean square.  o and dv of units longer than four chunks also carry
+the one rounding of the state that they read, elementwise and independent, so rho of the part from
+the state; two such roundings add to sqrt(2) rho < 2^-8.  Everything else before the output is held to
+2^-16 (operands split into two bf16 terms) or better, so 2^-8 + 2^-12 bounds the distance.  fp32 results are sums: each addition or product rounds by at most
 u = 2^-24, and an element of these cases passes through at most some 10^3 of them (64-token chunks
 summed by 16-term products, one decay and one addition of the state per chunk, the D-term products)
 whose errors are independent, so sqrt(10^3) u = 2e-6; F32_TOL = 4e-6 is twice that.  dg also
@@ -145,12 +147,17 @@ def test_split_and_whole_sequences_agree(gdn):
     for seg in (1, 2, 5, 14):
         o, ht = gdn.linattn_fwd(*args, x["h0"], seg_chunks=seg)
         got = gdn.linattn_bwd(*args, x["dout"], x["h0"], x["dht"], seg_chunks=seg)
-        # bf16 results differ where a last fp32 bit tips the rounding: by one step of 2^-8, rarely
-        assert ref.rel(o, whole[0]) <= 2.0 ** -10
+        # o and dv of long units round the state's elements to bf16, and of short units not: the two
+        # results differ by that rounding, at most 2^-8 of each element, rho = 2^-8 / sqrt 3 in the
+        # mean square and independent from element to element, so rho of the sum over the state's
+        # rows; and by the two roundings of the results, each rho again: sqrt(3) rho = 2^-8
+        assert ref.rel(o, whole[0]) <= 2.0 ** -8
+        assert ref.rel(got["dv"], gw["dv"]) <= 2.0 ** -8
         assert ref.rel(ht, whole[1]) <= F32_TOL
         assert ref.rel(got["dg"], gw["dg"]) <= DG_TOL
         assert ref.rel(got["dh0"], gw["dh0"]) <= F32_TOL
-        assert all(ref.rel(got[n], gw[n]) <= 2.0 ** -10 for n in ("dq", "dk", "dv"))
+        # these differ where a last fp32 bit tips the rounding: by one step of 2^-8, rarely
+        assert all(ref.rel(got[n], gw[n]) <= 2.0 ** -10 for n in ("dq", "dk"))
 
 
 def test_no_tokens(gdn):
