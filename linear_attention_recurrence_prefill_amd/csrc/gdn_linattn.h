@@ -47,6 +47,7 @@ struct LinArgs {
   // whole sequences (L = 0), at most kMaxLongestFirst: taken longest first, all heads of one before
   // the next, so that the last workgroups to start are the shortest
   int32_t longest_first;
+  int32_t cus;           // of the device
   float scale;
 };
 

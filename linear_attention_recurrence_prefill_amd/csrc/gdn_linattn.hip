@@ -243,33 +243,34 @@ constexpr size_t pass_lds_bytes() {
 
 }  // namespace
 
+template <int WAVES>
 struct PassShared {
   // the chunk's decays, by its parity: G (log2, hi + lo) and the factors of x's and y's rows
   __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
   // dg's parts, by the chunk's parity; the pairs' row sums (in the block on the diagonal, off it) and
   // the columns' sums over each wave's tiles
-  float dots[2][4][64], rsum[2][2][64], csum[2][4][32];
+  float dots[2][WAVES][64], rsum[2][2][64], csum[2][4][32];
   float s_decay[2];
   int unit[4];
 };
 
-template <class E, int D, int PASS>
-__device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShared &sh) {
+template <class E, int D, int PASS, int WAVES>
+__device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShared<WAVES> &sh) {
   typedef Op<E> X;
   typedef typename X::Frag Frag;
   typedef PassTraits<PASS> PT;
-  constexpr int NT = D / 64;      // 16-column tiles of the state per wave
+  constexpr int NT = D / (16 * WAVES);  // 16-column tiles of the state per wave
   constexpr int LDY = D + X::kPadYZ, LDX = D + X::kPadXW;
   constexpr int MT = D / 16;      // 16-row tiles of the state
   constexpr int KS = D / 32;      // products over a row
   constexpr int EPU = 16 / (int)sizeof(E);
   constexpr int UPR = D / EPU;            // 16-byte units per row
-  constexpr int UPT = 64 * UPR / 256;     // ... per thread and tile
+  constexpr int UPT = UPR / WAVES;        // ... per thread and tile
   // terms of the split operands (see the file's head)
   constexpr bool kB = sizeof(E) == 2;
   constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);  // ... at most, see state_terms
   constexpr int kPTerms = p_terms<E>();
-  constexpr int kDecayWave = 3;  // waves 0 to 2 form P
+  constexpr int kDecayWave = WAVES - 1;
 
   E *const ty = reinterpret_cast<E *>(smem);   // tiles of 64 rows
   E *const tz = ty + 64 * LDY;
@@ -390,7 +391,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   // lane holds one 32-bit offset per row stride, and rows past the sequence's end are out of the
   // buffer's range, so they read as zeros and are not written.
   const int r0 = tid / UPR, o0 = tid % UPR * EPU;
-  constexpr int kRows = 256 / UPR;  // rows per round
+  constexpr int kRows = 64 * WAVES / UPR;  // rows per round
   const auto rows_of = [&](const void *base, int64_t t0, int heads, int head, int n, int size) {
     const char *p = static_cast<const char *>(base) + (t0 * heads + head) * D * size;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), (short)0,
@@ -438,7 +439,9 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     if (!PT::kDots || w != kDecayWave) return;
     const int64_t t = t_beg + (int64_t)ch * kChunk + lane;
     float *const to = PASS == kLinDq ? a.dg_q : a.dg_k;
-    const float d = dots[par][0][lane] + dots[par][1][lane] + dots[par][2][lane] + dots[par][3][lane];
+    float d = dots[par][0][lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) d += dots[par][i][lane];
     if (t < t_end) to[(int64_t)h * a.T + t] = d;
     if (PASS == kLinDq) {
       // sum over the pairs s >= t > i = sum_{s >= t} (row sum - column sum); rows from the end.  The
@@ -507,7 +510,8 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       // the pairs within the chunk: P's ten 16 x 16 tiles, two or three per wave.  Waves 0 and 2: the
       // 32 x 32 blocks on the diagonal (two tiles masked within, one whole, one that is zero); waves
       // 1 and 3: 16 rows of x each of the block off it.
-      const bool diag = (w & 1) == 0;
+      // (Of eight waves, 4 to 7 go on to the state's share.)
+      const bool forms_p = WAVES == 4 || w < 4, diag = (w & 1) == 0;
       const int xb = diag ? 16 * w : PT::kRev ? 16 * (w >> 1) : 32 + 16 * (w >> 1);  // first row of x
       const int yb = diag ? 16 * w : PT::kRev ? 32 : 0;                             // ... of y
       f32x4 p[3];  // on the diagonal: (0, 0), the whole one, (1, 1); off it: y's two tiles
@@ -534,7 +538,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
           }
         }
       };
-      tiles(xrow, yrow, p);
+      if (forms_p) tiles(xrow, yrow, p);
       // p of rows xo + c of x and yo + 4 gq .. of y, decayed; masked: only pairs in order
       const auto decayed = [&](f32x4 v, int xo, int yo, bool masked) {
         const float xh = g_hi[xo + c], xl = g_lo[xo + c];
@@ -547,15 +551,15 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
         }
         return v;
       };
-      if (diag) {
+      if (forms_p && diag) {
         p[0] = decayed(p[0], xb, yb, true);
         p[1] = decayed(p[1], PT::kRev ? xb : xb + 16, PT::kRev ? yb + 16 : yb, false);
         p[2] = decayed(p[2], xb + 16, yb + 16, true);
-      } else {
+      } else if (forms_p) {
         p[0] = decayed(p[0], xb, yb, false);
         p[1] = decayed(p[1], xb, yb + 16, false);
       }
-      if (PASS == kLinDq) {  // pairs strictly apart: (q . k) (do . v) decayed, by rows and columns
+      if (PASS == kLinDq && forms_p) {  // pairs strictly apart: (q . k) (do . v) decayed, by rows and columns
         f32x4 m[3];
         sched_fence();
         tiles(wrow, zrow, m);
@@ -610,7 +614,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
           store_tile(xt, yt + 1, p[1]);
         }
       };
-      if (!PT::kDots) store_p();
+      if (!PT::kDots && forms_p) store_p();
 
       // the state's share: 32 rows of the state at a time, split once for the four row tiles, with
       // the next 32 rows' operands read during the products
@@ -668,7 +672,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       read_z();
       lds_barrier();
       if (PT::kDots) {
-        store_p();
+        if (forms_p) store_p();
         if (it + 1 < nsteps) fetch(in, ch + step);
         lds_barrier();
       }
@@ -822,7 +826,12 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
     __syncthreads();  // the last chunk's parts have been read
     if (lane == 0) dots[0][w][0] = (float)d;
     __syncthreads();
-    if (tid == 0) a.unit_dot[uh] = dots[0][0][0] + dots[0][1][0] + dots[0][2][0] + dots[0][3][0];
+    if (tid == 0) {
+      float sum = dots[0][0][0];
+#pragma unroll
+      for (int i = 1; i < WAVES; ++i) sum += dots[0][i][0];
+      a.unit_dot[uh] = sum;
+    }
   }
 }
 
@@ -841,19 +850,19 @@ constexpr size_t stage_lds_bytes() {
   }
 }
 
-template <class E, int D, int WHAT>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void lin_stage_kernel(LinArgs a) {
+template <class E, int D, int WHAT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, sizeof(E) == 2 || WAVES == 8 ? 2 : 1) void lin_stage_kernel(LinArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  __shared__ PassShared sh;
+  __shared__ PassShared<WAVES> sh;
   if constexpr (WHAT == kGroupSums) {
-    if (blockIdx.z == 0) lin_pass<E, D, kLinSumFwd>(a, smem, sh);
-    else lin_pass<E, D, kLinSumRev>(a, smem, sh);
+    if (blockIdx.z == 0) lin_pass<E, D, kLinSumFwd, WAVES>(a, smem, sh);
+    else lin_pass<E, D, kLinSumRev, WAVES>(a, smem, sh);
   } else if constexpr (WHAT == kGroupGrads) {
-    if (blockIdx.z == 0) lin_pass<E, D, kLinDq>(a, smem, sh);
-    else if (blockIdx.z == 1) lin_pass<E, D, kLinDk>(a, smem, sh);
-    else lin_pass<E, D, kLinDv>(a, smem, sh);
+    if (blockIdx.z == 0) lin_pass<E, D, kLinDq, WAVES>(a, smem, sh);
+    else if (blockIdx.z == 1) lin_pass<E, D, kLinDk, WAVES>(a, smem, sh);
+    else lin_pass<E, D, kLinDv, WAVES>(a, smem, sh);
   } else {
-    lin_pass<E, D, WHAT>(a, smem, sh);
+    lin_pass<E, D, WHAT, WAVES>(a, smem, sh);
   }
 }
 
@@ -1032,10 +1041,9 @@ __global__ __launch_bounds__(256) void lin_zero_kernel(float *x, int64_t n) {
     x[i] = 0.f;
 }
 
-template <class E, int D, int WHAT>
-hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
+template <class E, int D, int WHAT, int WAVES>
+hipError_t launch_stage(const LinArgs &a, int kinds, hipStream_t stream) {
   constexpr size_t lds = stage_lds_bytes<E, D, WHAT>();
-  constexpr int kinds = WHAT == kGroupSums ? 2 : WHAT == kGroupGrads ? 3 : 1;
   if (lds > 65536) {  // above the default limit of dynamic LDS, which is raised once per device
     static std::atomic<uint64_t> raised{0};
     int dev = 0;
@@ -1043,16 +1051,36 @@ hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const uint64_t bit = (uint64_t)1 << (dev & 63);
     if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_stage_kernel<E, D, WHAT>),
+      e = hipFuncSetAttribute(reinterpret_cast<const void *>(&lin_stage_kernel<E, D, WHAT, WAVES>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
       if (dev <= 63) raised.fetch_or(bit, std::memory_order_relaxed);
     }
   }
   const unsigned u = (unsigned)a.units, h = (unsigned)a.H;
-  hipLaunchKernelGGL((lin_stage_kernel<E, D, WHAT>),
-                     a.longest_first ? dim3(h, u, kinds) : dim3(u, h, kinds), dim3(256), lds, stream, a);
+  hipLaunchKernelGGL((lin_stage_kernel<E, D, WHAT, WAVES>),
+                     a.longest_first ? dim3(h, u, kinds) : dim3(u, h, kinds), dim3(64 * WAVES), lds,
+                     stream, a);
   return hipGetLastError();
+}
+
+// Waves per workgroup, d = 128: a workgroup that has a CU to itself takes eight, with 16 columns of
+// the state each (8K packed tokens x 8 heads, 237 workgroups: 64 to 57 us; fp32, 4K tokens: 84 to
+// 77 us, always alone on its CU); where two of four waves share a CU eight are slower (65K tokens,
+// backward: 660 against 780 us), since P is still formed by four.
+template <class E, int D, int WHAT>
+hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
+  constexpr int kinds = WHAT == kGroupSums ? 2 : WHAT == kGroupGrads ? 3 : 1;
+  if constexpr (D == 64) {
+    return launch_stage<E, D, WHAT, 4>(a, kinds, stream);
+  } else if constexpr (sizeof(E) == 4) {
+    return launch_stage<E, D, WHAT, 8>(a, kinds, stream);
+  } else {
+    // about that many: the last unit of a sequence is on average half a unit
+    const int64_t units = a.L > 0 ? (a.T / kChunk) / a.L + (a.N + 1) / 2 : a.N;
+    return units * a.H * kinds <= a.cus ? launch_stage<E, D, WHAT, 8>(a, kinds, stream)
+                                        : launch_stage<E, D, WHAT, 4>(a, kinds, stream);
+  }
 }
 
 template <int WHAT>

@@ -123,7 +123,7 @@ gdn_status layout(const gdn_linattn_problem *p, bool bwd, Layout *l) {
   return GDN_OK;
 }
 
-gdn::LinArgs base_args(const gdn_linattn_problem *p, const Layout &l, const void *q, const void *k,
+gdn::LinArgs base_args(const gdn_linattn_problem *p, const Layout &l, int cus, const void *q, const void *k,
                        const void *v, const float *g, const int32_t *cu, const float *h0, char *ws) {
   gdn::LinArgs a{};
   a.q = q;
@@ -141,6 +141,7 @@ gdn::LinArgs base_args(const gdn_linattn_problem *p, const Layout &l, const void
   a.L = l.L;
   a.units = l.units;
   a.longest_first = l.L == 0 && p->num_seqs > 1 && p->num_seqs <= gdn::kMaxLongestFirst;
+  a.cus = cus;
   a.scale = p->scale;
   if (l.L > 0) {
     a.unit_s = reinterpret_cast<float *>(ws + l.unit_s);
@@ -213,7 +214,8 @@ gdn_status gdn_linattn_fwd(const gdn_linattn_problem *p, const void *q, const vo
                 {q, k, v, h0, o, ht});
   if (s == GDN_OK && T > 0) s = check_all("q, k, v and o", {q, k, v, o}, {});
   if (s != GDN_OK) return s;
-  s = device_info(nullptr);
+  int cus = 0;
+  s = device_info(&cus);
   if (s != GDN_OK) return s;
   if (T == 0) {  // every sequence is empty: its final state is its initial state
     if (!ht) return GDN_OK;
@@ -235,7 +237,7 @@ gdn_status gdn_linattn_fwd(const gdn_linattn_problem *p, const void *q, const vo
     s = debug_validate(cu_seqlens, p->num_seqs, T, nullptr, stream);
     if (s != GDN_OK) return s;
   }
-  gdn::LinArgs a = base_args(p, l, q, k, v, g, cu_seqlens, h0, static_cast<char *>(workspace));
+  gdn::LinArgs a = base_args(p, l, cus, q, k, v, g, cu_seqlens, h0, static_cast<char *>(workspace));
   a.o = o;
   a.ht = ht;
   LAUNCH(gdn::launch_linattn_fwd(a, p->head_dim, p->dtype == GDN_DTYPE_BF16, stream),
@@ -258,7 +260,8 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
   if (s == GDN_OK && T > 0)
     s = check_all("q, k, v, dout, dq, dk and dv", {q, k, v, dout, dq, dk, dv}, {});
   if (s != GDN_OK) return s;
-  s = device_info(nullptr);
+  int cus = 0;
+  s = device_info(&cus);
   if (s != GDN_OK) return s;
   const int64_t H = p->num_heads, D = p->head_dim;
   const bool shared = p->h0_seq_stride == 0;
@@ -287,7 +290,7 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
     if (s != GDN_OK) return s;
   }
   char *ws = static_cast<char *>(workspace);
-  gdn::LinArgs a = base_args(p, l, q, k, v, g, cu_seqlens, h0, ws);
+  gdn::LinArgs a = base_args(p, l, cus, q, k, v, g, cu_seqlens, h0, ws);
   a.dout = dout;
   a.dht = dht;
   if (l.L > 0) a.unit_r = reinterpret_cast<float *>(ws + l.unit_r);
