@@ -254,7 +254,9 @@ struct PassShared {
   int unit[4];
 };
 
-template <class E, int D, int PASS, int WAVES>
+// SETS: chunks whose rows are on their way in registers (sums: one or two; two set launch bounds that
+// hold two workgroups per CU, one three).
+template <class E, int D, int PASS, int WAVES, int SETS>
 __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShared<WAVES> &sh) {
   typedef Op<E> X;
   typedef typename X::Frag Frag;
@@ -379,9 +381,9 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
       }
     }
 
-  // rows that are on their way, and their log decays (one wave): the next chunk's, in the sums the
-  // next two chunks' (their rounds are short against a load's latency)
-  constexpr int kSets = PT::kSum ? 2 : 1;
+  // rows that are on their way, and their log decays (one wave): the next chunk's, or the next two
+  // chunks' (the sums' rounds are short against a load's latency)
+  constexpr int kSets = SETS;
   struct Rows {
     u32x4 y[UPT], z[UPT], x[UPT], w[UPT];
     float g;
@@ -503,7 +505,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 #pragma unroll
         for (int t = 0; t < NT; ++t) zf[kb][t] = X::template column<LDY>(tz + 32 * kb * LDY + 4 * t, z_at);
     };
-    if constexpr (PT::kSum) read_z();
+    if constexpr (PT::kSum && kSets > 1) read_z();
 
     f32x4 o[4][NT];  // the output by 16-row tiles
     if constexpr (!PT::kSum) {
@@ -741,6 +743,10 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const f32x4 fa = lds_f32x4(f_y + 32 * kb + 4 * gq), fb = lds_f32x4(f_y + 32 * kb + 16 + 4 * gq);
+      if constexpr (PT::kSum && kSets == 1) {  // here: fewer registers through the round
+#pragma unroll
+        for (int t = 0; t < NT; ++t) zf[kb][t] = X::template column<LDY>(tz + 32 * kb * LDY + 4 * t, z_at);
+      }
       Frag b1[NT], b2[NT], b3[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -850,19 +856,25 @@ constexpr size_t stage_lds_bytes() {
   }
 }
 
+// Three workgroups per CU: the forward's sums of d = 128, with one chunk's rows on their way (32K
+// tokens x 8 heads, whole forward: 134 to 130 us).  Those of the backward, twice as many units at
+// once, are faster two by two with two chunks' rows each (65K tokens: 660 against 674 us).
 template <class E, int D, int WHAT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(E) == 2 || WAVES == 8 ? 2 : 1) void lin_stage_kernel(LinArgs a) {
+constexpr bool kThree = sizeof(E) == 2 && D == 128 && WHAT == kLinSumFwd && WAVES == 4;
+
+template <class E, int D, int WHAT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, (kThree<E, D, WHAT, WAVES> ? 3 : sizeof(E) == 2 || WAVES == 8 ? 2 : 1)) void lin_stage_kernel(LinArgs a) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   __shared__ PassShared<WAVES> sh;
   if constexpr (WHAT == kGroupSums) {
-    if (blockIdx.z == 0) lin_pass<E, D, kLinSumFwd, WAVES>(a, smem, sh);
-    else lin_pass<E, D, kLinSumRev, WAVES>(a, smem, sh);
+    if (blockIdx.z == 0) lin_pass<E, D, kLinSumFwd, WAVES, 2>(a, smem, sh);
+    else lin_pass<E, D, kLinSumRev, WAVES, 2>(a, smem, sh);
   } else if constexpr (WHAT == kGroupGrads) {
-    if (blockIdx.z == 0) lin_pass<E, D, kLinDq, WAVES>(a, smem, sh);
-    else if (blockIdx.z == 1) lin_pass<E, D, kLinDk, WAVES>(a, smem, sh);
-    else lin_pass<E, D, kLinDv, WAVES>(a, smem, sh);
+    if (blockIdx.z == 0) lin_pass<E, D, kLinDq, WAVES, 1>(a, smem, sh);
+    else if (blockIdx.z == 1) lin_pass<E, D, kLinDk, WAVES, 1>(a, smem, sh);
+    else lin_pass<E, D, kLinDv, WAVES, 1>(a, smem, sh);
   } else {
-    lin_pass<E, D, WHAT, WAVES>(a, smem, sh);
+    lin_pass<E, D, WHAT, WAVES, (kThree<E, D, WHAT, WAVES> || WHAT != kLinSumFwd ? 1 : 2)>(a, smem, sh);
   }
 }
 
