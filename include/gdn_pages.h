@@ -10,7 +10,7 @@
  * that a call cannot take sets a fault flag (gdn_device_faults: 2 a page outside its pool or a
  * parent that is not live, 4 a page that one call would write twice or both read and write, 8 no
  * free page; debug mode returns GDN_ERR_DEVICE_CHECK) and its entry is left out; the others are
- * done.  Calls on one pool are ordered by their stream.
+ * done.  Lists and flags of one call do not overlap.  Calls on one pool are ordered by their stream.
  */
 #ifndef GDN_PAGES_H_
 #define GDN_PAGES_H_
@@ -22,12 +22,12 @@ extern "C" {
 #endif
 
 /* Bytes of device workspace that any call below needs for a pool of num_pages pages (of pages_copy:
- * 0) and lists of `count` entries.  Host only. */
+ * dst's) and lists of `count` entries.  Host only. */
 gdn_status gdn_pages_workspace_size(int32_t num_pages, int32_t count, size_t *bytes);
 
 /* dst[dst_pages[i]] = src[src_pages[i]] for i < count.  src_pages[i] = -1 writes zeros,
  * dst_pages[i] = -1 skips the pair.  dst and src are one pool or do not overlap.  Of pairs with the
- * same destination the first is done; in one pool a pair whose source is another pair's destination
+ * same destination (and pages in range) the first is done; in one pool a pair whose source is another pair's destination
  * is left out. */
 gdn_status gdn_pages_copy(void *dst, int32_t dst_num_pages, const void *src, int32_t src_num_pages,
                           int64_t page_bytes, const int32_t *dst_pages, const int32_t *src_pages,

@@ -373,6 +373,10 @@ gdn_status check_pool(const char *what, const void *pool, int32_t num_pages, int
   return GDN_OK;
 }
 
+bool overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+  return a < b + m && b < a + n;
+}
+
 gdn_status check_workspace(int32_t num_pages, int32_t count, const void *ws, size_t bytes) {
   size_t need = 0;
   gdn_status s = gdn_pages_workspace_size(num_pages, count, &need);
@@ -386,8 +390,8 @@ gdn_status check_workspace(int32_t num_pages, int32_t count, const void *ws, siz
 gdn_status gdn_pages_workspace_size(int32_t num_pages, int32_t count, size_t *bytes) {
   if (!bytes) return fail(GDN_ERR_NULL_ARG, "bytes is NULL");
   if (num_pages < 0 || count < 0) return fail(GDN_ERR_BAD_SHAPE, "num_pages and count must be >= 0");
-  // the free list or the moves (two lists of at most half the pages, and their number), or a
-  // copy's two lists
+  // the free list, the moves (two lists of at most half the pages, and their number) or each
+  // destination's first pair; a copy's two lists
   *bytes = align_up(sizeof(int32_t) * ((size_t)num_pages + 4)) + align_up(sizeof(int32_t) * 2 * (size_t)count);
   return GDN_OK;
 }
@@ -406,15 +410,16 @@ gdn_status gdn_pages_copy(void *dst, int32_t dst_num_pages, const void *src, int
     return fail(GDN_ERR_BAD_SHAPE, "dst and src must be one pool or not overlap");
   if (count == 0) return GDN_OK;
   s = check_all("dst_pages and src_pages", {dst_pages, src_pages}, {});
-  if (s == GDN_OK) s = check_workspace(0, count, workspace, workspace_bytes);
+  if (s == GDN_OK) s = check_workspace(dst_num_pages, count, workspace, workspace_bytes);
   if (s != GDN_OK) return s;
   int cus = 0;
   s = device_info(&cus);
   if (s == GDN_OK) s = clear_faults_for_debug(stream);
   if (s != GDN_OK) return s;
   int32_t *const to = static_cast<int32_t *>(workspace), *const from = to + count;
+  int32_t *const first = from + count;
   LAUNCH(gdn::launch_pages_check(dst_pages, src_pages, count, dst_num_pages, src_num_pages, same, to,
-                                 from, fault_word(), stream),
+                                 from, first, fault_word(), stream),
          "pages_copy: checks");
   gdn::PageCopyArgs a{static_cast<char *>(dst), c, dst_num_pages, src_num_pages, page_bytes,
                       to, from, count, nullptr};
@@ -432,6 +437,9 @@ gdn_status gdn_pages_fork(void *pool, int32_t *live, int32_t num_pages, int64_t 
   s = check_all("live, parents and children", {live, parents, children}, {});
   if (s == GDN_OK) s = check_workspace(num_pages, 0, workspace, workspace_bytes);
   if (s != GDN_OK) return s;
+  if (overlap(children, count, parents, count) || overlap(children, count, live, num_pages) ||
+      overlap(parents, count, live, num_pages))
+    return fail(GDN_ERR_BAD_SHAPE, "live, parents and children must not overlap");
   int cus = 0;
   s = device_info(&cus);
   if (s == GDN_OK) s = clear_faults_for_debug(stream);
@@ -452,6 +460,8 @@ gdn_status gdn_pages_free(int32_t *live, int32_t num_pages, const int32_t *pages
   if (count == 0) return GDN_OK;
   gdn_status s = check_all("live and pages", {live, pages}, {});
   if (s != GDN_OK) return s;
+  if (overlap(live, num_pages, pages, count))
+    return fail(GDN_ERR_BAD_SHAPE, "live and pages must not overlap");
   s = device_info(nullptr);
   if (s == GDN_OK) s = clear_faults_for_debug(stream);
   if (s != GDN_OK) return s;
@@ -466,6 +476,8 @@ gdn_status gdn_pages_compact(void *pool, int32_t *live, int32_t num_pages, int64
   if (s == GDN_OK) s = check_all("live and remap", {live, remap}, {});
   if (s == GDN_OK) s = check_workspace(num_pages, 0, workspace, workspace_bytes);
   if (s != GDN_OK) return s;
+  if (overlap(live, num_pages, remap, num_pages))
+    return fail(GDN_ERR_BAD_SHAPE, "live and remap must not overlap");
   int cus = 0;
   s = device_info(&cus);
   if (s == GDN_OK) s = clear_faults_for_debug(stream);

@@ -16,10 +16,11 @@ struct PageCopyArgs {
   const int32_t *count_dev;      // when not null, the number of pairs, at most count
 };
 
-// to[i], from[i] of the pairs that can be copied at once, -1 to of the others (see gdn_pages_copy).
+// to[i], from[i] of the pairs that can be copied at once, -1 to of the others (see gdn_pages_copy);
+// first: scratch, [dst_pages].
 hipError_t launch_pages_check(const int32_t *dst_idx, const int32_t *src_idx, int32_t count,
                               int32_t dst_pages, int32_t src_pages, bool same_pool, int32_t *to,
-                              int32_t *from, uint32_t *faults, hipStream_t stream);
+                              int32_t *from, int32_t *first, uint32_t *faults, hipStream_t stream);
 hipError_t launch_pages_copy(const PageCopyArgs &a, int cus, hipStream_t stream);
 // children[i] = the pages that take parents[i] (-1: none), marked in live; free_list: [num_pages].
 hipError_t launch_pages_fork_plan(int32_t *live, int32_t num_pages, const int32_t *parents,

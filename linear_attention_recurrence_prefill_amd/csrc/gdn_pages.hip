@@ -38,26 +38,48 @@ __global__ __launch_bounds__(256) void pages_copy_kernel(PageCopyArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void pages_check_kernel(const int32_t *__restrict__ dst_idx,
-                                                          const int32_t *__restrict__ src_idx,
-                                                          int count, int dst_pages, int src_pages,
-                                                          bool same_pool, int32_t *to,
-                                                          int32_t *from, uint32_t *faults) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= count) return;
-  const int32_t d = dst_idx[i], s = src_idx[i];
-  uint32_t f = 0u;
-  if (d < -1 || d >= dst_pages || s < -1 || s >= src_pages) f = kFaultPageRange;
-  bool twice = false, hazard = false;
-  for (int j = 0; j < count; ++j) {
-    const int32_t e = dst_idx[j];
-    twice |= j < i && e == d;
-    hazard |= same_pool && j != i && e == s;
+// The pairs of a copy that can be done at once: first[d] is the first pair that names destination d.
+// Linear in the list, whatever the pools' size: only the entries that a pair names are set.
+__global__ __launch_bounds__(kPlanThreads) void pages_check_kernel(const int32_t *dst_idx,
+                                                                   const int32_t *src_idx, int count,
+                                                                   int dst_pages, int src_pages,
+                                                                   bool same_pool, int32_t *to,
+                                                                   int32_t *from, int32_t *first,
+                                                                   uint32_t *faults) {
+  const auto in_range = [&](int32_t d, int32_t s) {
+    return d >= -1 && d < dst_pages && s >= -1 && s < src_pages;
+  };
+  for (int64_t i = threadIdx.x; i < count; i += kPlanThreads) {
+    const int32_t d = dst_idx[i], s = src_idx[i];
+    if (!in_range(d, s)) continue;
+    if (d >= 0) first[d] = INT32_MAX;
+    if (same_pool && s >= 0) first[s] = INT32_MAX;
   }
-  if (f == 0u && d >= 0 && (twice || (hazard && s >= 0))) f = kFaultPageTwice;
-  to[i] = f || d < 0 || (same_pool && d == s) ? -1 : d;
-  from[i] = f ? -1 : s;
-  if (f && faults) atomicOr(faults, f);
+  __threadfence();
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < count; i += kPlanThreads) {
+    const int32_t d = dst_idx[i], s = src_idx[i];
+    if (in_range(d, s) && d >= 0) atomicMin(first + d, (int32_t)i);
+  }
+  __threadfence();
+  __syncthreads();
+  const auto first_of = [&](int32_t d) {  // past the caches that the stores above went through
+    return __hip_atomic_load(first + d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  for (int64_t i = threadIdx.x; i < count; i += kPlanThreads) {
+    const int32_t d = dst_idx[i], s = src_idx[i];
+    uint32_t f = 0u;
+    if (!in_range(d, s)) {
+      f = kFaultPageRange;
+    } else if (d >= 0) {
+      bool races = first_of(d) != i;
+      if (same_pool && s >= 0 && s != d) races |= first_of(s) != INT32_MAX;
+      if (races) f = kFaultPageTwice;
+    }
+    to[i] = f || d < 0 || (same_pool && d == s) ? -1 : d;
+    from[i] = f ? -1 : s;
+    if (f && faults) atomicOr(faults, f);
+  }
 }
 
 // Inclusive sum of x over the workgroup; *all gets the total.  Every thread calls it.
@@ -158,9 +180,9 @@ __global__ __launch_bounds__(kPlanThreads) void pages_compact_plan_kernel(int32_
 
 hipError_t launch_pages_check(const int32_t *dst_idx, const int32_t *src_idx, int32_t count,
                               int32_t dst_pages, int32_t src_pages, bool same_pool, int32_t *to,
-                              int32_t *from, uint32_t *faults, hipStream_t stream) {
-  hipLaunchKernelGGL(pages_check_kernel, dim3((count + 255) / 256), dim3(256), 0, stream, dst_idx,
-                     src_idx, count, dst_pages, src_pages, same_pool, to, from, faults);
+                              int32_t *from, int32_t *first, uint32_t *faults, hipStream_t stream) {
+  hipLaunchKernelGGL(pages_check_kernel, dim3(1), dim3(kPlanThreads), 0, stream, dst_idx, src_idx,
+                     count, dst_pages, src_pages, same_pool, to, from, first, faults);
   return hipGetLastError();
 }
 

@@ -57,7 +57,7 @@ def pages_copy(dst, src, dst_pages, src_pages, *, workspace=None):
     lib = load_library()
     n = dst_pages.numel()
     with _on(dst.device):
-        ws = _workspace(workspace, pages_workspace_bytes(0, n), dst.device)
+        ws = _workspace(workspace, pages_workspace_bytes(P, n), dst.device)
         _check(lib.gdn_pages_copy(_at(dst), P, _at(src), Ps, nbytes, _at(dst_pages),
                                   _at(src_pages), n, _at(ws), _nbytes(ws),
                                   _stream_of(dst.device)))
@@ -73,8 +73,6 @@ def pages_fork(pool, live, parents, *, children=None, workspace=None):
     _index("parents", parents)
     if children is not None:
         _index("children", children, tuple(parents.shape))
-        if children.data_at() == parents.data_at() and parents.numel():
-            raise ValueError("children must not overlap parents")
     _same_device(pool.device, live=live, parents=parents, children=children)
     lib = load_library()
     with _on(pool.device):

@@ -66,6 +66,35 @@ def test_copy_refuses_pairs_that_race(gdn):
     assert torch.equal(dst, keep) and gdn.device_faults(clear=True) == 4
 
 
+@pytest.mark.parametrize("same", [True, False])
+def test_copy_of_long_lists(gdn, same):
+    """Lists beyond one round of the checking workgroup, with pages named often and bad pages."""
+    rng = random.Random(11)
+    P, n = 700, 2500
+    src = pool_of(P, (8,), seed=12)
+    dst = src if same else pool_of(P, (8,), seed=13)
+    to = [rng.choice([-1, P, rng.randrange(P)]) for _ in range(n)]
+    frm = [rng.choice([-1, rng.randrange(P), rng.randrange(-2, P + 1)]) for _ in range(n)]
+    if same:  # half of the pages are sources only
+        to = [t - t % 2 if 0 <= t < P else t for t in to]
+        frm = [f if rng.random() < 0.1 or not 0 <= f < P else f | 1 for f in frm]
+    ok = [-1 <= t < P and -1 <= f < P for t, f in zip(to, frm)]
+    written, want, faults = {}, dst.clone(), 0
+    for i, t in enumerate(to):
+        if ok[i] and t >= 0:
+            written.setdefault(t, i)
+    for i, (t, f) in enumerate(zip(to, frm)):
+        if not ok[i]:
+            faults |= 2
+        elif t >= 0 and (written[t] != i or (same and f >= 0 and f != t and f in written)):
+            faults |= 4
+        elif t >= 0:
+            want[t] = src[f] if f >= 0 else 0
+    gdn.device_faults(clear=True)
+    gdn.pages_copy(dst, src, ints(to), ints(frm))
+    assert torch.equal(dst, want) and gdn.device_faults(clear=True) == faults
+
+
 def fork_ref(pool, live, parents):
     pool, live, children = pool.clone(), list(live), []
     free = [p for p, x in enumerate(live) if not x]
@@ -101,6 +130,19 @@ def test_fork(gdn, P, n, seed):
     bad = 2 if any(p >= 0 and not live[p] for p in parents) else 0
     full = 8 if sum(p == -1 or live[p] != 0 for p in parents) > sum(not x for x in live) else 0
     assert gdn.device_faults(clear=True) == bad | full
+
+
+def test_fork_into_a_given_list(gdn):
+    pool, lv, kids = pool_of(4, (8,)), ints([1, 0, 1, 0]), ints([9, 9, 9])
+    assert gdn.pages_fork(pool, lv, ints([2, 0, 0]), children=kids) is kids
+    assert kids.tolist() == [1, 3, -1] and lv.tolist() == [1, 1, 1, 1]
+    assert torch.equal(pool[1], pool[2]) and torch.equal(pool[3], pool[0])
+    assert gdn.device_faults(clear=True) == 8
+    for bad in (kids, kids[:2]):  # the list itself, and a part of it
+        with pytest.raises(RuntimeError, match="overlap"):
+            gdn.pages_fork(pool, lv, kids[1:] if bad is not kids else kids, children=bad)
+    with pytest.raises(RuntimeError, match="overlap"):
+        gdn.pages_free(lv, lv[1:])
 
 
 def test_fork_of_pages_outside_the_pool(gdn):

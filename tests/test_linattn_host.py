@@ -182,6 +182,13 @@ def test_pages_are_checked(lib):
         lib.gdn_pages_compact(pool, live, P, nb, remap, ws, wb, None)  # noqa: E731
     assert comp(pool=None) == 1 and comp(live=None) == 1 and comp(remap=None) == 1
     assert comp(P=0) == 2 and comp(nb=40) == 2 and comp(wb=0) == 6
+    # lists and flags of one call overlap
+    at = lambda i: ctypes.c_void_p((1 << 22) + 4 * i)  # noqa: E731
+    assert fork(live=at(0), P=4, par=at(8), kids=at(9), n=2) == 2
+    assert fork(live=at(0), P=4, par=at(8), kids=at(3), n=2) == 2
+    assert fork(live=at(0), P=4, par=at(3), kids=at(8), n=2) == 2
+    assert comp(live=at(0), P=4, remap=at(3)) == 2
+    assert lib.gdn_pages_free(at(0), 4, at(3), 2, None) == 2
 
 
 def test_binding_refuses_bad_tensors():
