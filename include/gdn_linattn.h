@@ -74,7 +74,7 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
  *   pages == NULL: state is [batch, H, d, d], row b's state is state[b] (num_pages is not used).
  *   pages: device int32 [batch]; state is a pool [num_pages, H, d, d] and row b's state is
  *     state[pages[b]].  -1 marks a row without a sequence (padding): its o is zero.  A page
- *     outside the pool, or one that an earlier row has, is treated as -1 and sets a fault flag
+ *     outside the pool, or one that an earlier row has (at most 2^16 rows), is treated as -1 and sets a fault flag
  *     (gdn_device_faults bits 2 and 4; in debug mode the call returns GDN_ERR_DEVICE_CHECK). */
 gdn_status gdn_linattn_step(int32_t batch, int32_t num_heads, int32_t num_k_heads,
                             int32_t head_dim, int32_t dtype, int32_t head_decay, float scale,

@@ -987,7 +987,6 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(LinArgs a) {
     };
     for (int hi = c1; hi > c0; hi -= 64) {  // chunks [lo, hi)
       const int lo = max(c0, hi - 64), n = hi - lo;
-#pragma unroll 4
       for (int j = w; j < n; j += 4) {
         const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane;
         F2 all;
@@ -999,7 +998,6 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(LinArgs a) {
       const F2 x = lane < n ? sums[lane] : F2{0.f, 0.f};
       F2 whole;
       const F2 after = add2(from_here(x, whole), F2{-x.hi, -x.lo});
-#pragma unroll 2
       for (int j = w; j < n; j += 4) {
         const int64_t t = t_beg + (int64_t)(lo + j) * kChunk + lane;
         const bool in = t < t_end;
@@ -1038,9 +1036,13 @@ __global__ __launch_bounds__(256) void lin_dg_head_kernel(LinArgs a) {
 }
 
 template <class E>
-__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *__restrict__ part, int64_t n4,
-                                                            int G, int D4, E *__restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *__restrict__ part,
+                                                            const int32_t *cu, int N, int64_t T,
+                                                            int HK, int G, int D4,
+                                                            E *__restrict__ out) {
+  // rows of no sequence have no parts and stay as they are
+  const int64_t row = (int64_t)HK * D4, i0 = max(cu[0], 0) * row, i1 = min((int64_t)cu[N], T) * row;
+  for (int64_t i = i0 + (int64_t)blockIdx.x * 256 + threadIdx.x; i < i1; i += (int64_t)gridDim.x * 256) {
     const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + i / D4 * G * D4 + i % D4;
     f32x4 s = p[0];
     for (int j = 1; j < G; ++j) s += p[(int64_t)j * D4];
@@ -1136,16 +1138,17 @@ hipError_t launch_linattn_bwd(const LinArgs &a, int D, bool is_bf16, hipStream_t
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_group_sum(const float *part, int64_t T, int32_t H, int32_t HK, int32_t D,
-                                    bool is_bf16, void *out, hipStream_t stream) {
-  const int64_t n4 = T * HK * D / 4, blocks = std::min<int64_t>((n4 + 255) / 256, 16384);
+hipError_t launch_linattn_group_sum(const float *part, const LinArgs &a, int D, bool is_bf16, void *out,
+                                    hipStream_t stream) {
+  const int64_t n4 = a.T * a.HK * D / 4;
+  const unsigned blocks = (unsigned)std::min<int64_t>((n4 + 255) / 256, 16384);
   if (n4 <= 0) return hipSuccess;
   if (is_bf16)
-    hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, dim3((unsigned)blocks), dim3(256), 0, stream,
-                       part, n4, H / HK, D / 4, static_cast<bf16 *>(out));
+    hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, dim3(blocks), dim3(256), 0, stream, part, a.cu, a.N,
+                       a.T, a.HK, a.H / a.HK, D / 4, static_cast<bf16 *>(out));
   else
-    hipLaunchKernelGGL(lin_group_sum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, stream,
-                       part, n4, H / HK, D / 4, static_cast<float *>(out));
+    hipLaunchKernelGGL(lin_group_sum_kernel<float>, dim3(blocks), dim3(256), 0, stream, part, a.cu, a.N,
+                       a.T, a.HK, a.H / a.HK, D / 4, static_cast<float *>(out));
   return hipGetLastError();
 }
 

@@ -17,8 +17,11 @@ using namespace gdn::api;
 
 namespace {
 
-// Workgroups of 256 threads along a grid's first dimension stay below 2^32 threads.
-constexpr int64_t kMaxUnits = (int64_t)1 << 24;
+// Workgroups of at most 512 threads along a grid's first dimension stay below 2^32 threads.
+constexpr int64_t kMaxUnits = (int64_t)1 << 23;
+// Rows of a step on pages: each looks for its page in the rows before it (2^16 rows: 256 loads per
+// thread).
+constexpr int32_t kMaxPagedRows = 1 << 16;
 
 gdn_status check_problem(const gdn_linattn_problem *p) {
   if (!p) return fail(GDN_ERR_NULL_ARG, "problem is NULL");
@@ -310,9 +313,9 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
   a.dh0 = dh0 && shared ? reinterpret_cast<float *>(ws + l.dh0_seq) : dh0;
   LAUNCH(gdn::launch_linattn_bwd(a, D, bf, stream), "linear attention backward");
   if (grouped) {
-    LAUNCH(gdn::launch_linattn_group_sum(dq_part, T, p->num_heads, k_heads(p), D, bf, dq, stream),
+    LAUNCH(gdn::launch_linattn_group_sum(dq_part, a, D, bf, dq, stream),
            "linear attention: dq of shared heads");
-    LAUNCH(gdn::launch_linattn_group_sum(dk_part, T, p->num_heads, k_heads(p), D, bf, dk, stream),
+    LAUNCH(gdn::launch_linattn_group_sum(dk_part, a, D, bf, dk, stream),
            "linear attention: dk of shared heads");
   }
   if (dh0 && shared)
@@ -327,7 +330,7 @@ gdn_status gdn_linattn_step(int32_t batch, int32_t num_heads, int32_t num_k_head
                             const int32_t *pages, int32_t num_pages, float *state, void *o,
                             hipStream_t stream) {
   if (batch < 1 || num_heads < 1 || (int64_t)batch * num_heads >= kMaxUnits)
-    return fail(GDN_ERR_BAD_SHAPE, "batch and num_heads must be >= 1, and their product below 2^24");
+    return fail(GDN_ERR_BAD_SHAPE, "batch and num_heads must be >= 1, and their product below 2^23");
   if (num_k_heads < 0 || num_k_heads > num_heads ||
       (num_k_heads > 0 && num_heads % num_k_heads != 0))
     return fail(GDN_ERR_BAD_SHAPE, "num_k_heads must be 0 or a divisor of num_heads");
@@ -336,6 +339,8 @@ gdn_status gdn_linattn_step(int32_t batch, int32_t num_heads, int32_t num_k_head
   if (head_decay != 0 && head_decay != 1) return fail(GDN_ERR_BAD_MODE, "head_decay must be 0 or 1");
   if (!std::isfinite(scale)) return fail(GDN_ERR_BAD_SHAPE, "scale must be finite");
   if (pages && num_pages < 1) return fail(GDN_ERR_BAD_SHAPE, "num_pages must be >= 1");
+  if (pages && batch > kMaxPagedRows)
+    return fail(GDN_ERR_BAD_SHAPE, "at most %d rows of a step have pages", kMaxPagedRows);
   gdn_status s = check_all("q, k, v, g, state and o", {q, k, v, g, state, o}, {q, k, v, state, o});
   if (s != GDN_OK) return s;
   s = device_info(nullptr);

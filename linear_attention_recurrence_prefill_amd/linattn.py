@@ -140,7 +140,7 @@ def linattn_fwd(q, k, v, g, cu_seqlens, h0=None, *, scale=1.0, seg_chunks=0, num
         _no_overlap("out", out, *ins)
     if final_state is not None:
         _check_out("final_state", final_state, (N, H, D, D), torch.float32, device)
-        _no_overlap("final_state", final_state, *ins)
+        _no_overlap("final_state", final_state, out, *ins)
     lib = load_library()
     with _on(device):
         nbytes = _workspace_bytes(lib.gdn_linattn_fwd_workspace_size, p)

@@ -11,6 +11,7 @@ summed by 16-term products, one decay and one addition of the state per chunk, t
 whose errors are independent, so sqrt(10^3) u = 2e-6; F32_TOL = 4e-6 is twice that.  dg also
 cancels: it is a difference of sums of |q . dq| and |k . dk| over up to a unit's tokens, held to
 2e-5 (the same count for the two sums, an order of magnitude for the cancellation)."""
+import ctypes
 import itertools
 
 import pytest
@@ -92,6 +93,62 @@ def test_long_sequences_in_units(gdn, dtype, D, seg):
     """Documents of many units, with a ragged end, and one unit exactly full."""
     x = ref.inputs([64 * 6, 701, 5], 2, 1, D, dtype, "token", "own", True, seed=12)
     run_both(gdn, x, dtype, 1.0, seg_chunks=seg)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,seg", [([450, 70], 0), ([450, 70], 2), ([450, 70], 1000), ([130, 0, 1], 1)])
+def test_many_heads(gdn, lens, seg, D):
+    """More workgroups than CUs in every stage: two heads of the reference, 140 times over."""
+    x = ref.inputs(lens, 2, 2, D, "bf16", "token", "own", True, seed=22)
+    r, tol = host64(x), tols("bf16")
+    rargs = [r[n] for n in ("q", "k", "v", "g", "cu")]
+    o_ref, ht_ref = ref.forward(*rargs, r["h0"], 0.5)
+    want = ref.backward(*rargs, r["dout"], r["h0"], r["dht"], 0.5)
+    many = lambda t: t.repeat(*(140 if i == 1 else 1 for i in range(t.dim())))  # noqa: E731
+    d = dev({n: t if n == "cu" else many(t) for n, t in x.items()})
+    args = [d[n] for n in ("q", "k", "v", "g", "cu")]
+    o, ht = gdn.linattn_fwd(*args, d["h0"], scale=0.5, seg_chunks=seg)
+    check("o", o, many(o_ref), tol["o"])
+    check("ht", ht, many(ht_ref), tol["ht"])
+    got = gdn.linattn_bwd(*args, d["dout"], d["h0"], d["dht"], scale=0.5, seg_chunks=seg)
+    for n in want:
+        check(n, got[n], many(want[n]), tol[n])
+
+
+@pytest.mark.parametrize("Hk", [4, 2])
+@pytest.mark.parametrize("seg", [1, 1000])
+def test_rows_of_no_sequence_stay(gdn, Hk, seg):
+    """Tokens after the last sequence: outputs there are left as they were, and NaN in their inputs
+    reaches nothing."""
+    x = ref.inputs([70, 100], 4, Hk, 64, "bf16", "token", "none", False, seed=23)
+    pad = lambda t: torch.cat([t, torch.full_like(t[:9], float("nan"))])  # noqa: E731
+    d = dev(x)
+    names = ("q", "k", "v", "g", "dout")
+    w = {n: pad(d[n]) for n in names}
+    cu = d["cu"]
+    o, ht = gdn.linattn_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], seg_chunks=seg)
+    got = gdn.linattn_bwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["dout"], seg_chunks=seg)
+    out = torch.full_like(w["v"], 7.0)
+    o2, ht2 = gdn.linattn_fwd(w["q"], w["k"], w["v"], w["g"], cu, out=out, seg_chunks=seg)
+    assert torch.equal(o2[:170], o) and torch.equal(ht2, ht)
+    assert (o2[170:] == 7).all()
+    lib = gdn.load_library()
+    from linear_attention_recurrence_prefill_amd.linattn import _at, _problem
+
+    p, device, N, H, D = _problem(w["q"], w["k"], w["v"], w["g"], cu, None, 1.0, seg, 0)
+    res = {"d" + n: torch.full_like(w[n], 7.0) for n in ("q", "k", "v", "g")}
+    dh0 = torch.empty(N, H, D, D, device=device)
+    ws = torch.empty(gdn.gdn_linattn_bwd_workspace_size(w["q"], w["k"], w["v"], w["g"], cu, seg_chunks=seg),
+                     dtype=torch.uint8, device=device)
+    status = lib.gdn_linattn_bwd(ctypes.byref(p), *(_at(w[n]) for n in ("q", "k", "v", "g")), _at(cu),
+                                 None, _at(w["dout"]), None,
+                                 *(_at(res[n]) for n in ("dq", "dk", "dv", "dg")), _at(dh0), _at(ws),
+                                 ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0 and torch.equal(dh0, got["dh0"])
+    for n, t in res.items():
+        assert torch.equal(t[:170], got[n]), n
+        assert (t[170:] == 7).all(), n
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

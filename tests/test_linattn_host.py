@@ -152,6 +152,8 @@ def test_step_pointers(lib):
         a[i] = ODD
         assert lib.gdn_linattn_step(*ok, *a[:5], 4, *a[5:], None) == 7, i
     assert lib.gdn_linattn_step(*ok, *[FAKE] * 5, 0, FAKE, FAKE, None) == 2
+    assert lib.gdn_linattn_step(1 << 16 | 1, 1, *ok[2:], *[FAKE] * 5, 4, FAKE, FAKE, None) == 2
+    assert lib.gdn_linattn_step(1 << 22, 2, *ok[2:], *[FAKE] * 4, None, 0, FAKE, FAKE, None) == 2
     assert lib.gdn_linattn_step(4, 8, 0, 128, 1, 0, float("nan"), *[FAKE] * 5, 4, FAKE, FAKE, None) == 2
 
 
