@@ -207,6 +207,18 @@ __device__ __forceinline__ float kept(float x, int d) {
   return __int_as_float(__float_as_int(x) & ((d - 1) >> 31));
 }
 
+// Sums over the wave's four rows of 16 lanes, of two values at once: the halves of a and b are
+// exchanged (lanes 32 and up of a with the others of b), so one addition adds both over the halves,
+// a's in lanes 0 to 31; the same again by rows.
+__device__ __forceinline__ float halves_sum(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float rows_sum(float a, float b) {  // rows 0, 2: a's pairs of rows; 1, 3: b's
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 template <int PASS>
 struct PassTraits {
   static constexpr bool kSum = PASS == kLinSumFwd || PASS == kLinSumRev;
@@ -249,7 +261,8 @@ struct PassShared {
   __attribute__((aligned(16))) float s_hi[2][64], s_lo[2][64], s_x[2][64], s_yf[2][64];
   // dg's parts, by the chunk's parity; the pairs' row sums (in the block on the diagonal, off it) and
   // the columns' sums over each wave's tiles
-  float dots[2][WAVES][64], rsum[2][2][64], csum[2][4][32];
+  __attribute__((aligned(16))) float csum[2][4][32];
+  float dots[2][WAVES][64], rsum[2][2][64];
   float s_decay[2];
   int unit[4];
 };
@@ -565,7 +578,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
         f32x4 m[3];
         sched_fence();
         tiles(wrow, zrow, m);
-        float cs[2][4];
+        f32x4 cs[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float m0 = m[0][j] * p[0][j], m1 = m[1][j] * p[1][j];
@@ -582,19 +595,15 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = row16_sum_dpp(cs[k][j]);
-            if (c == 0) csum[par][w][16 * k + 4 * gq + j] = x;
-          }
+          for (int j = 0; j < 4; ++j) cs[k][j] = row16_sum_dpp(cs[k][j]);
+        if (c == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          r_sum[i] += __shfl_xor(r_sum[i], 16, 64);
-          r_sum[i] += __shfl_xor(r_sum[i], 32, 64);
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<f32x4 *>(&csum[par][w][16 * k + 4 * gq]) = cs[k];
         }
-        if (gq == 0) {
-          rsum[par][w & 1][xb + c] = r_sum[0];
-          if (diag) rsum[par][0][xb + 16 + c] = r_sum[1];
-        }
+        const float half = halves_sum(r_sum[0], r_sum[1]), sum = rows_sum(half, half);
+        if (gq == 0) rsum[par][w & 1][xb + c] = sum;
+        if (gq == 2 && diag) rsum[par][0][xb + 16 + c] = sum;
       }
       const auto store_tile = [&](int xt, int yt, f32x4 v) {
         E *const to = tp + (p_slot<PT::kRev>(xt, yt) * kPTerms * 64 + lane) * 4;
@@ -652,6 +661,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
         }
         sched_fence();
       }
+      float d_sum[4];
 #pragma unroll
       for (int xt = 0; xt < 4; ++xt) {
         const int xr = 16 * xt + c;
@@ -666,11 +676,12 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
 #pragma unroll
             for (int j = 0; j < 4; ++j) d += wv[j] * o[xt][t][j];
           }
-          d += __shfl_xor(d, 16, 64);
-          d += __shfl_xor(d, 32, 64);
-          if (gq == 0) dots[par][w][xr] = d;
+          d_sum[xt] = d;
         }
       }
+      if (PT::kDots)  // rows of lanes 0 to 3: row tiles 0, 2, 1, 3
+        dots[par][w][32 * (gq & 1) + 16 * (gq >> 1) + c] =
+            rows_sum(halves_sum(d_sum[0], d_sum[1]), halves_sum(d_sum[2], d_sum[3]));
       read_z();
       lds_barrier();
       if (PT::kDots) {
