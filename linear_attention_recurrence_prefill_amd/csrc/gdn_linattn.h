@@ -57,9 +57,9 @@ inline int linattn_blocks_per_cu(int D, bool bf16) { return bf16 || D == 64 ? 2 
 hipError_t launch_linattn_fwd(const LinArgs &a, int D, bool bf16, hipStream_t stream);
 // The backward: the same in both directions, dq, dk, dv and dg's parts, then dg.
 hipError_t launch_linattn_bwd(const LinArgs &a, int D, bool bf16, hipStream_t stream);
-// out[t, hk] = sum over the H / HK value heads of part[t, h] for the tokens t of a's sequences, fp32
-// to the input type.
-hipError_t launch_linattn_group_sum(const float *part, const LinArgs &a, int D, bool bf16, void *out,
+// dq[t, hk] = sum over the H / HK value heads of a.dq[t, h] (fp32) for the tokens t of a's sequences,
+// to the input type, and dk likewise.
+hipError_t launch_linattn_group_sum(const LinArgs &a, int D, bool bf16, void *dq, void *dk,
                                     hipStream_t stream);
 hipError_t launch_linattn_zero(float *x, int64_t n, hipStream_t stream);
 

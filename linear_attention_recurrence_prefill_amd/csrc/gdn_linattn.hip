@@ -1046,14 +1046,16 @@ __global__ __launch_bounds__(256) void lin_dg_head_kernel(LinArgs a) {
   if (threadIdx.x == 0) a.dg[h] = (float)(part[0] + part[1] + part[2] + part[3]);
 }
 
+// dq (grid y = 0) and dk of key heads from their value heads' shares.
 template <class E>
-__global__ __launch_bounds__(256) void lin_group_sum_kernel(const float *__restrict__ part,
-                                                            const int32_t *cu, int N, int64_t T,
-                                                            int HK, int G, int D4,
-                                                            E *__restrict__ out) {
+__global__ __launch_bounds__(256) void lin_group_sum_kernel(LinArgs a, int D4, E *dq, E *dk) {
+  const float *const part = static_cast<const float *>(blockIdx.y == 0 ? a.dq : a.dk);
+  E *const out = blockIdx.y == 0 ? dq : dk;
+  const int G = a.H / a.HK;
   // rows of no sequence have no parts and stay as they are
-  const int64_t row = (int64_t)HK * D4, i0 = max(cu[0], 0) * row, i1 = min((int64_t)cu[N], T) * row;
-  for (int64_t i = i0 + (int64_t)blockIdx.x * 256 + threadIdx.x; i < i1; i += (int64_t)gridDim.x * 256) {
+  const int64_t row = (int64_t)a.HK * D4, i1 = min((int64_t)a.cu[a.N], a.T) * row;
+  for (int64_t i = max(a.cu[0], 0) * row + (int64_t)blockIdx.x * 256 + threadIdx.x; i < i1;
+       i += (int64_t)gridDim.x * 256) {
     const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + i / D4 * G * D4 + i % D4;
     f32x4 s = p[0];
     for (int j = 1; j < G; ++j) s += p[(int64_t)j * D4];
@@ -1149,17 +1151,17 @@ hipError_t launch_linattn_bwd(const LinArgs &a, int D, bool is_bf16, hipStream_t
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_group_sum(const float *part, const LinArgs &a, int D, bool is_bf16, void *out,
+hipError_t launch_linattn_group_sum(const LinArgs &a, int D, bool is_bf16, void *dq, void *dk,
                                     hipStream_t stream) {
   const int64_t n4 = a.T * a.HK * D / 4;
-  const unsigned blocks = (unsigned)std::min<int64_t>((n4 + 255) / 256, 16384);
   if (n4 <= 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<int64_t>((n4 + 255) / 256, 16384), 2);
   if (is_bf16)
-    hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, dim3(blocks), dim3(256), 0, stream, part, a.cu, a.N,
-                       a.T, a.HK, a.H / a.HK, D / 4, static_cast<bf16 *>(out));
+    hipLaunchKernelGGL(lin_group_sum_kernel<bf16>, grid, dim3(256), 0, stream, a, D / 4,
+                       static_cast<bf16 *>(dq), static_cast<bf16 *>(dk));
   else
-    hipLaunchKernelGGL(lin_group_sum_kernel<float>, dim3(blocks), dim3(256), 0, stream, part, a.cu, a.N,
-                       a.T, a.HK, a.H / a.HK, D / 4, static_cast<float *>(out));
+    hipLaunchKernelGGL(lin_group_sum_kernel<float>, grid, dim3(256), 0, stream, a, D / 4,
+                       static_cast<float *>(dq), static_cast<float *>(dk));
   return hipGetLastError();
 }
 

@@ -312,12 +312,9 @@ gdn_status gdn_linattn_bwd(const gdn_linattn_problem *p, const void *q, const vo
   a.dv = dv;
   a.dh0 = dh0 && shared ? reinterpret_cast<float *>(ws + l.dh0_seq) : dh0;
   LAUNCH(gdn::launch_linattn_bwd(a, D, bf, stream), "linear attention backward");
-  if (grouped) {
-    LAUNCH(gdn::launch_linattn_group_sum(dq_part, a, D, bf, dq, stream),
-           "linear attention: dq of shared heads");
-    LAUNCH(gdn::launch_linattn_group_sum(dk_part, a, D, bf, dk, stream),
-           "linear attention: dk of shared heads");
-  }
+  if (grouped)
+    LAUNCH(gdn::launch_linattn_group_sum(a, D, bf, dq, dk, stream),
+           "linear attention: dq and dk of shared heads");
   if (dh0 && shared)
     LAUNCH(gdn::launch_sum_dh0(a.dh0, p->num_seqs, p->num_heads, D, dh0, stream),
            "linear attention: dh0 of a shared state");
