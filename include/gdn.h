@@ -261,7 +261,8 @@ gdn_status gdn_validate_cu_seqlens(const int32_t *cu_seqlens, int32_t num_seqs,
 
 /* Debug mode on (1) or off (0) for the whole process; its initial value comes from the
  * environment variable GDN_DEBUG (unset or "0": off).  In debug mode gdn_chunk_fwd,
- * gdn_chunk_fwd_intermediates, gdn_chunk_fwd_plan and gdn_chunk_bwd validate cu_seqlens on the
+ * gdn_chunk_fwd_intermediates, gdn_chunk_fwd_plan, gdn_chunk_bwd, gdn_linattn_fwd and
+ * gdn_linattn_bwd validate cu_seqlens on the
  * device (and compare it with cu_seqlens_host when one is given) before their first launch and
  * synchronise the stream (so they are not asynchronous,
  * and calls that overlap on one device share its check words).  No passage applies: a
@@ -270,7 +271,8 @@ gdn_status gdn_set_debug(int32_t on);
 int32_t gdn_get_debug(void);
 
 /* The current device's fault flags: bit 1 means a forward launch's bounded wait between its
- * waves ran out (its results are not to be trusted).  Synchronises the device, then copies the
+ * waves ran out (its results are not to be trusted); bits 2, 4 and 8 are those of gdn_pages.h and
+ * of gdn_linattn_step (a page that a call could not take).  Synchronises the device, then copies the
  * flags to *flags (host) and clears them when clear != 0.  No passage applies: a diagnostic of
  * this library's kernels. */
 gdn_status gdn_device_faults(uint32_t *flags, int32_t clear);

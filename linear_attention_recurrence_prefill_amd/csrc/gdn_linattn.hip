@@ -9,20 +9,32 @@
 // run backward in time on (q, do), and dv_t = dS_t^T k_t, dk_t = dS_t v_t.  So one kernel does all
 // of them (LinPass).  Nothing couples the columns of the state, and sequences are split into units
 // of L chunks exactly: a unit's own sum from zero (kLinSum*), the sums joined along the sequence
-// (lin_scan_kernel), the unit run from its true start.
+// (lin_scan_kernel), the unit run from its true start.  The backward's passes of one stage are one
+// launch (kGroupSums, kGroupGrads).
 //
-// Work of one workgroup (4 waves): one (unit, head).  Wave w owns D / 4 columns of the state, all D
-// rows of them, in MFMA accumulators: in that layout (lane n + 16 (m / 4), item m % 4)
-// two stacked 16-row tiles are, as they stand, the operand of a 16x16x32 product over the rows, in
-// the row order {4 gq + j, 16 + 4 gq + j}.  All row operands are read in that order, so neither
-// the state nor the 64 x 64 products P ever pass through LDS, and waves meet only at the tile
-// buffers.  P is formed by every wave (40 of its some 200 MFMAs per chunk).  Output tiles are
-// formed transposed (columns by items), so a lane stores 16 consecutive bytes of a row.
+// Work of one workgroup (4 waves, 8 where it has a CU to itself): one (unit, head).  Wave w owns
+// D / 4 (or D / 8) columns of the state, all D rows of them, in MFMA accumulators: in that layout
+// (lane n + 16 (m / 4), item m % 4) two stacked 16-row tiles are, as they stand, the operand of a
+// 16x16x32 product over the rows, in the row order {4 gq + j, 16 + 4 gq + j}.  All row operands are
+// read in that order, so the state never passes through LDS.  The masked 64 x 64 products P are
+// formed once per workgroup, ten 16 x 16 tiles over four waves, and pass through LDS in operand
+// order.  Output tiles are formed transposed (columns by items), so a lane stores 16 consecutive
+// bytes of a row.
 //
 // Rounding: inputs are bf16, sums and states fp32.  Products take bf16 operands; what is not an
 // input is split into a sum of bf16 terms: two terms (2^-17) where the result is rounded to bf16
-// in the end, three (2^-25) where it is kept in fp32 (final states, state gradients, dg's parts).
+// in the end, three (2^-25) where it is kept in fp32 (final states, state gradients, dg's parts);
+// one for the state that o and dv of units of more than kShortUnit chunks read (state_terms below).
 // fp32 inputs use the fp32 MFMA throughout.
+//
+// What bounds it (one MI355X, d = 128, bf16).  200K tokens x 16 heads forward: 0.79 ms for 3.36 GB,
+// 4.3 TB/s; the kernel's loads and stores alone take 0.73 ms there, its products on rows that stay
+// in the caches 0.67 ms.  65K tokens x 8 heads backward: sums 159, scan 21, gradients 559, dg 17 us;
+// the gradients alone move 2.0 GB (3.6 TB/s), but the same passes without HBM take as long: per SIMD
+// the matrix unit is busy 30 % of the time, vector issue 29 % (without MFMA), LDS 33 %, and two
+// waves per SIMD (256 registers each) overlap them only in part.  Fewer vector instructions
+// (decays folded into the state's share: 64 of some 900 per chunk) and passes of one unit placed
+// side by side on one XCD (677 against 661 us) did not shorten it.
 //
 // Decays: G in units of log2, accumulated as a pair of floats (hi + lo), and only differences of G
 // are exponentiated, so no factor overflows and far tokens keep their precision.  Log decays below
@@ -42,7 +54,7 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinLog2 = -512.f;
-constexpr int kShortUnit = 4;        // chunks
+constexpr int kShortUnit = 4;       // chunks, see state_terms
 constexpr float kNoDecay = -150.f;  // 2^-150 rounds to zero in fp32
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLog2eLo = 1.925963033500e-8f;  // log2(e) - kLog2e
@@ -895,7 +907,8 @@ namespace {
 // than one unit, S <- decay_u S + sum_u, written where unit u + 1's sum was.  rev: the gradients at
 // the units' ends, from the last unit to the first.  One thread per four elements of a state, its
 // loads kAhead units ahead of the chain: a chain's step is a few instructions, so the time is that
-// of the bytes in flight.
+// of the bytes in flight (65K tokens x 8 heads, both directions, 138 MB: 21 us, 6.5 TB/s; one chain
+// of 63 units x 8 heads, 67 MB: 21 us; 32 units ahead change neither).
 constexpr int kAhead = 16, kScanThreads = 128;
 
 template <bool REV>
@@ -955,7 +968,7 @@ __global__ __launch_bounds__(kScanThreads) void lin_scan_kernel(LinArgs a, int D
 // no cancelling terms; the scan's terms are of the size of dg near them, and it restarts at every
 // unit's end.  One workgroup per (unit, head), from the unit's end by blocks of 64 chunks: the waves
 // sum their chunks side by side, then finish them with the sums of the later ones.  A token whose
-// decay is zero in fp32 has no gradient.
+// decay is zero in fp32 has no gradient.  (65K tokens x 8 heads: 17 us.)
 __device__ __forceinline__ F2 lane_of(F2 x, int l) {
   return F2{__shfl(x.hi, l, 64), __shfl(x.lo, l, 64)};
 }

