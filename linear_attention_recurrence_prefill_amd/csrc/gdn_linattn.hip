@@ -30,8 +30,8 @@
 // What bounds it (one MI355X, d = 128, bf16).  200K tokens x 16 heads forward: 0.79 ms for 3.36 GB,
 // 4.3 TB/s; the kernel's loads and stores alone take 0.73 ms there, its products on rows that stay
 // in the caches 0.67 ms.  65K tokens x 8 heads backward: sums 159, scan 21, gradients 559, dg 17 us;
-// the gradients alone move 2.0 GB (3.6 TB/s), but the same passes without HBM take as long: per SIMD
-// the matrix unit is busy 30 % of the time, vector issue 29 % (without MFMA), LDS 33 %, and two
+// the gradients alone move 2.05 GB (3.7 TB/s), but the same passes without HBM take as long: per SIMD
+// the matrix unit is busy 31 % of the time, vector issue 30 % (without MFMA), LDS 33 %, and two
 // waves per SIMD (256 registers each) overlap them only in part.  Fewer vector instructions
 // (decays folded into the state's share: 64 of some 900 per chunk) and passes of one unit placed
 // side by side on one XCD (677 against 661 us) did not shorten it.
@@ -907,8 +907,8 @@ namespace {
 // than one unit, S <- decay_u S + sum_u, written where unit u + 1's sum was.  rev: the gradients at
 // the units' ends, from the last unit to the first.  One thread per four elements of a state, its
 // loads kAhead units ahead of the chain: a chain's step is a few instructions, so the time is that
-// of the bytes in flight (65K tokens x 8 heads, both directions, 138 MB: 21 us, 6.5 TB/s; one chain
-// of 63 units x 8 heads, 67 MB: 21 us; 32 units ahead change neither).
+// of the bytes in flight (65K tokens x 8 heads, both directions, 124 MB: 21 us, 5.8 TB/s; one chain
+// of 63 units x 8 heads, 59 MB: 21 us; 32 units ahead change neither).
 constexpr int kAhead = 16, kScanThreads = 128;
 
 template <bool REV>
