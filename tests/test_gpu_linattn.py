@@ -413,6 +413,53 @@ def test_on_a_stream_of_its_own(gdn):
     assert all(torch.equal(gb[n], wb[n]) for n in wb)
 
 
+def test_two_calls_at_once(gdn):
+    """Calls on two streams, each with its own workspace, as each alone (bitwise: nothing is shared)."""
+    xs = [dev(ref.inputs([900, 333], 3, 3, 64, "bf16", "token", "own", True, seed=s)) for s in (31, 32)]
+
+    def call(x):
+        args = [x[n] for n in ("q", "k", "v", "g", "cu")]
+        o, ht = gdn.linattn_fwd(*args, x["h0"], seg_chunks=2)
+        return dict(gdn.linattn_bwd(*args, x["dout"], x["h0"], x["dht"], seg_chunks=2), o=o, ht=ht)
+
+    alone = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    both = [[], []]
+    for _ in range(5):
+        for i, (x, st) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(st):
+                both[i].append(call(x))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for got in both[i]:
+            assert all(torch.equal(got[n], alone[i][n]) for n in alone[i])
+
+
+def test_offsets_past_32_bits(gdn):
+    """Tensors of more than 2^32 bytes: the last heads' results are those of the last heads alone."""
+    T, H, D = 140001, 128, 128
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, k, v, dout = (rnd(T, H, D) for _ in range(4))
+    q.mul_(D ** -0.5)
+    k.mul_(D ** -0.5)
+    g = -0.1 * torch.rand(T, H, generator=gen, device="cuda")
+    cu = torch.tensor([0, 100000, T], dtype=torch.int32, device="cuda")
+    few = [t[:, -2:].contiguous() for t in (q, k, v, g)]
+    o, ht = gdn.linattn_fwd(q, k, v, g, cu, seg_chunks=64)
+    of, htf = gdn.linattn_fwd(*few, cu, seg_chunks=64)
+    assert ref.rel(o[:, -2:], of) <= 2.0 ** -10 and ref.rel(ht[:, -2:], htf) <= F32_TOL
+    assert ref.rel(o[-70:, -1], of[-70:, -1]) <= 2.0 ** -10
+    got = gdn.linattn_bwd(q, k, v, g, cu, dout, seg_chunks=64)
+    want = gdn.linattn_bwd(*few, cu, dout[:, -2:].contiguous(), seg_chunks=64)
+    for n in ("dq", "dk", "dv"):
+        assert ref.rel(got[n][:, -2:], want[n]) <= 2.0 ** -10, n
+        assert ref.rel(got[n][-70:, -1], want[n][-70:, -1]) <= 2.0 ** -10, n
+    assert ref.rel(got["dg"][:, -2:], want["dg"]) <= DG_TOL
+    assert ref.rel(got["dh0"][:, -2:], want["dh0"]) <= F32_TOL
+
+
 def test_graph_replays(gdn):
     """Forward, backward and steps captured into two graphs, replayed on new inputs with eager
     calls between the replays."""
