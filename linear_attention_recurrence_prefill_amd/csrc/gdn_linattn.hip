@@ -496,8 +496,9 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && final_state != nullptr));
   // Terms of the state in the outputs o and dv: one in longer units.  Its rounding, 2^-9 of each
   // element, adds to the output's own of the same size (1.65e-3 becomes at most 2.3e-3 in the mean
-  // square) and takes a tenth off the pass (200K tokens x 16 heads: 0.90 to 0.81 ms); in units of a
-  // few chunks, which wait for memory and each other anyway, it would cost accuracy for nothing.
+  // square) and takes a tenth off the pass (200K tokens x 16 heads: 0.90 to 0.81 ms); units of a few
+  // chunks keep two terms, which cost them little (2K tokens x 8 heads 32 us either way, 16K tokens in
+  // units of four chunks 93 against 90 us).
   const int state_terms = PT::kDots || nsteps <= kShortUnit ? kStateTerms : 1;
   if (nsteps > 0) {
     fetch(set[0], ch);

