@@ -111,7 +111,8 @@ def fork_ref(pool, live, parents):
     return pool, live, children
 
 
-@pytest.mark.parametrize("P,n,seed", [(1, 1, 0), (6, 3, 1), (40, 25, 2), (40, 60, 3), (2500, 1300, 4)])
+@pytest.mark.parametrize("P,n,seed", [(1, 1, 0), (6, 3, 1), (40, 25, 2), (40, 60, 3), (2500, 1300, 4),
+                                      (1024, 1024, 5), (1024, 1025, 6), (1025, 30, 7)])
 def test_fork(gdn, P, n, seed):
     """Fewer and more parents than free pages, the same parent many times, new (zero) pages, parents
     that are not live; a pool beyond one round of the planning workgroup."""
@@ -172,7 +173,8 @@ def test_free(gdn):
     (1, 0.0, (4,), torch.float32), (1, 1.0, (4,), torch.float32), (2, 0.5, (4,), torch.float32),
     (33, 0.4, (1028,), torch.float32), (64, 0.0, (8,), torch.float32),
     (64, 1.0, (8,), torch.float32), (65, 0.6, (9, 1000), torch.bfloat16),
-    (2600, 0.5, (8,), torch.float32)])
+    (2600, 0.5, (8,), torch.float32), (1024, 0.5, (8,), torch.float32),
+    (1024, 1.0, (8,), torch.float32), (1024, 0.0, (8,), torch.float32), (1025, 0.7, (8,), torch.float32)])
 def test_compact(gdn, P, share, shape, dtype):
     rng = random.Random(P)
     live = [int(rng.random() < share) for _ in range(P)]
