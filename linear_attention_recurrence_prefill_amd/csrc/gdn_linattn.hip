@@ -23,8 +23,10 @@
 //
 // Rounding: inputs are bf16, sums and states fp32.  Products take bf16 operands; what is not an
 // input is split into a sum of bf16 terms: two terms (2^-17) where the result is rounded to bf16
-// in the end, three (2^-25) where it is kept in fp32 (final states, state gradients, dg's parts);
-// one for the state that o and dv of units of more than kShortUnit chunks read (state_terms below).
+// in the end, three (2^-25) where it is kept in fp32 (final states, state gradients, dg's parts).
+// One term of the state is not enough for o and dv: its rounding goes with the size of the terms
+// q_i S_ij, not of their sum, which is far smaller where keys share a direction that the query does
+// not (keys of weight 4 in one direction against unit noise: 8.5e-2 of o, two terms 1.7e-3).
 // fp32 inputs use the fp32 MFMA throughout.
 //
 // What bounds it (one MI355X, d = 128, bf16).  200K tokens x 16 heads forward: 0.79 ms for 3.36 GB,
@@ -54,7 +56,6 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinLog2 = -512.f;
-constexpr int kShortUnit = 4;       // chunks, see state_terms
 constexpr float kNoDecay = -150.f;  // 2^-150 rounds to zero in fp32
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLog2eLo = 1.925963033500e-8f;  // log2(e) - kLog2e
@@ -295,7 +296,7 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   constexpr int UPT = UPR / WAVES;        // ... per thread and tile
   // terms of the split operands (see the file's head)
   constexpr bool kB = sizeof(E) == 2;
-  constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);  // ... at most, see state_terms
+  constexpr int kStateTerms = !kB ? 1 : (PT::kDots ? 3 : 2);
   constexpr int kPTerms = p_terms<E>();
   constexpr int kDecayWave = WAVES - 1;
 
@@ -494,12 +495,6 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
   const int nsteps = c1 - c0;
   // terms of the state update: three where the state is written out or feeds dg
   const bool precise = kB && (PT::kSum || PT::kDots || (edge_out && final_state != nullptr));
-  // Terms of the state in the outputs o and dv: one in longer units.  Its rounding, 2^-9 of each
-  // element, adds to the output's own of the same size (1.65e-3 becomes at most 2.3e-3 in the mean
-  // square) and takes a tenth off the pass (200K tokens x 16 heads: 0.90 to 0.81 ms); units of a few
-  // chunks keep two terms, which cost them little (2K tokens x 8 heads 32 us either way, 16K tokens in
-  // units of four chunks 93 against 90 us).
-  const int state_terms = PT::kDots || nsteps <= kShortUnit ? kStateTerms : 1;
   if (nsteps > 0) {
     fetch(set[0], ch);
     if (kSets > 1 && nsteps > 1) fetch(set[kSets - 1], ch + step);
@@ -663,7 +658,6 @@ __device__ __forceinline__ void lin_pass(const LinArgs &a, char *smem, PassShare
         for (int t = 0; t < NT; ++t) s0[t] = S[2 * ks][t], s1[t] = S[2 * ks + 1][t];
 #pragma unroll
         for (int i = 0; i < kStateTerms; ++i) {
-          if (i > 0 && i >= state_terms) break;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             const Frag sf = X::round(s0[t], s1[t]);
