@@ -26,9 +26,9 @@ extern "C" {
 gdn_status gdn_pages_workspace_size(int32_t num_pages, int32_t count, size_t *bytes);
 
 /* dst[dst_pages[i]] = src[src_pages[i]] for i < count.  src_pages[i] = -1 writes zeros,
- * dst_pages[i] = -1 skips the pair.  dst and src are one pool or do not overlap.  Of pairs with the
- * same destination (and pages in range) the first is done; in one pool a pair whose source is another pair's destination
- * is left out. */
+ * dst_pages[i] = -1 skips the pair.  dst and src are one pool (the same address; the page counts may
+ * differ) or do not overlap.  Of pairs with the same destination (and pages in range) the first is
+ * done; in one pool a pair whose source is another pair's destination is left out. */
 gdn_status gdn_pages_copy(void *dst, int32_t dst_num_pages, const void *src, int32_t src_num_pages,
                           int64_t page_bytes, const int32_t *dst_pages, const int32_t *src_pages,
                           int32_t count, void *workspace, size_t workspace_bytes,

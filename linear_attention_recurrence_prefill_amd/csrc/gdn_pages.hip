@@ -41,7 +41,9 @@ __global__ __launch_bounds__(256) void pages_copy_kernel(PageCopyArgs a) {
 }
 
 // The pairs of a copy that can be done at once: first[d] is the first pair that names destination d.
-// Linear in the list, whatever the pools' size: only the entries that a pair names are set.
+// Linear in the list, whatever the pools' size: only the entries that a pair names are set.  One pool
+// may be given with two page counts (a part of it as dst): `first` has an entry for each page of dst,
+// and a source page past them is no pair's destination.
 __global__ __launch_bounds__(kPlanThreads) void pages_check_kernel(const int32_t *dst_idx,
                                                                    const int32_t *src_idx, int count,
                                                                    int dst_pages, int src_pages,
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(kPlanThreads) void pages_check_kernel(const int32_t
     const int32_t d = dst_idx[i], s = src_idx[i];
     if (!in_range(d, s)) continue;
     if (d >= 0) first[d] = INT32_MAX;
-    if (same_pool && s >= 0) first[s] = INT32_MAX;
+    if (same_pool && s >= 0 && s < dst_pages) first[s] = INT32_MAX;
   }
   __threadfence();
   __syncthreads();
@@ -75,7 +77,7 @@ __global__ __launch_bounds__(kPlanThreads) void pages_check_kernel(const int32_t
       f = kFaultPageRange;
     } else if (d >= 0) {
       bool races = first_of(d) != i;
-      if (same_pool && s >= 0 && s != d) races |= first_of(s) != INT32_MAX;
+      if (same_pool && s >= 0 && s < dst_pages && s != d) races |= first_of(s) != INT32_MAX;
       if (races) f = kFaultPageTwice;
     }
     to[i] = f || d < 0 || (same_pool && d == s) ? -1 : d;

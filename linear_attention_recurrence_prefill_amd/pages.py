@@ -44,9 +44,9 @@ def pages_workspace_bytes(num_pages, count):
 
 def pages_copy(dst, src, dst_pages, src_pages, *, workspace=None):
     """dst[dst_pages[i]] = src[src_pages[i]]; a source of -1 writes zeros, a destination of -1 skips
-    the pair.  dst and src are one pool or do not overlap.  Of pairs with one destination the first
-    is done; in one pool a pair whose source is another pair's destination is left out.  Returns
-    dst."""
+    the pair.  dst and src are one pool (or the pool and its first pages) or do not overlap.  Of pairs
+    with one destination the first is done; in one pool a pair whose source is another pair's
+    destination is left out.  Returns dst."""
     P, nbytes = _pool("dst", dst)
     Ps, nb_src = _pool("src", src)
     if nb_src != nbytes or src.dtype != dst.dtype:
