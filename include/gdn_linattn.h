@@ -16,6 +16,11 @@
  *   g     fp32 log decays: [T, H], one for each token and head, or [H] with head_decay = 1 (a
  *         constant decay per head).  g <= 0 in use; -inf empties the state.  Values that are
  *         finite but whose decay is zero in fp32 act as -inf and get a zero gradient.
+ * Sums and states are fp32.  With bf16 inputs, what is not an input and enters a product (states,
+ * decayed rows, the masked products of a chunk) does so as a sum of bf16 terms: to 2^-16 of each
+ * element at least, to 2^-24 where the result stays fp32, whatever the units' length.  bf16 outputs
+ * are rounded once.  dg_t is a difference of sums over its unit: its error is absolute, fp32's
+ * rounding of the unit's |q_s . dq_s| and |k_s . dk_s|, not relative to a small dg_t.
  * Inputs are finite: a NaN or infinity in a token's k or v reaches the outputs of its own 64-token
  * chunk (also those before it) and of what follows in its sequence and head; no other sequence or
  * head.
@@ -39,7 +44,8 @@ typedef struct gdn_linattn_problem {
   int32_t dtype;         /* GDN_DTYPE_* of q, k, v, o and their gradients */
   int32_t head_decay;    /* 0: g is [T, H]; 1: g is [H] */
   int32_t seg_chunks;    /* length in chunks of the units that sequences are split into; 0 = chosen
-                          * from the sizes */
+                          * from T, N and H, so by the sequences' mean length: set it (8 or so) for
+                          * one long sequence among many short ones, which else is not split */
   int32_t num_slots;     /* workgroups that the choice plans for; 0 = the device's */
   float scale;           /* o_t = scale * S_t^T q_t */
   int32_t reserved;      /* must be 0 */

@@ -33,7 +33,7 @@ struct LinArgs {
   float *ht, *dh0;       // per sequence [N, H, D, D], or null
   // split runs (L > 0): per unit and head, the states at the unit's start (unit_s) and the state
   // gradients at its end (unit_r), [units, H, D, D]; before the scan they hold the unit's own
-  // contribution, with its whole decay in decay_s (decay_r: the same for the reversed sums)
+  // contribution, with its whole decay in unit_decay ([2, units, H]: forward and reversed sums)
   float *unit_s, *unit_r, *unit_decay;
   int32_t *seq_unit;     // [N]: each sequence's first unit
   // dg's parts: pairs within a chunk, q . dq and k . dk of the states' shares, [H, T] each, and
@@ -51,7 +51,9 @@ struct LinArgs {
   float scale;
 };
 
-// Workgroups of the passes that one CU holds at once (registers and LDS).
+// Workgroups of four waves that one CU holds at once (registers and LDS), which the units' length is
+// planned for.  Launches differ: one of eight waves where there are no more workgroups than CUs and in
+// fp32 with d = 128, three in the forward's sums with d = 128.
 inline int linattn_blocks_per_cu(int D, bool bf16) { return bf16 || D == 64 ? 2 : 1; }
 // The forward: the units' sums and the states at their starts (split runs), then the output.
 hipError_t launch_linattn_fwd(const LinArgs &a, int D, bool bf16, hipStream_t stream);

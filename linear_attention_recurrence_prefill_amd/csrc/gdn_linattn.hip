@@ -29,14 +29,14 @@
 // not (keys of weight 4 in one direction against unit noise: 8.5e-2 of o, two terms 1.7e-3).
 // fp32 inputs use the fp32 MFMA throughout.
 //
-// What bounds it (one MI355X, d = 128, bf16).  200K tokens x 16 heads forward: 0.79 ms for 3.36 GB,
-// 4.3 TB/s; the kernel's loads and stores alone take 0.73 ms there, its products on rows that stay
-// in the caches 0.67 ms.  65K tokens x 8 heads backward: sums 159, scan 21, gradients 559, dg 17 us;
-// the gradients alone move 2.05 GB (3.7 TB/s), but the same passes without HBM take as long: per SIMD
-// the matrix unit is busy 31 % of the time, vector issue 30 % (without MFMA), LDS 33 %, and two
-// waves per SIMD (256 registers each) overlap them only in part.  Fewer vector instructions
-// (decays folded into the state's share: 64 of some 900 per chunk) and passes of one unit placed
-// side by side on one XCD (677 against 661 us) did not shorten it.
+// What bounds it (one MI355X, d = 128, bf16).  200K tokens x 16 heads forward: 0.87 ms for 3.36 GB,
+// 3.9 TB/s; the kernel's loads and stores alone take 0.73 ms there, its products on rows that stay
+// in the caches 0.72 ms.  65K tokens x 8 heads backward: sums 159, scan 21, gradients 572, dg 17 us;
+// the gradients alone move 2.05 GB (3.6 TB/s), and on rows that stay in the caches they still take
+// 476 us: per SIMD the matrix unit is busy 32 % of the time, vector issue 31 % (without MFMA), LDS
+// 32 %, and two waves per SIMD (256 registers each) overlap them only in part.  Fewer vector
+// instructions (decays folded into the state's share: 64 of some 900 per chunk) and passes of one
+// unit placed side by side on one XCD (677 against 661 us) did not shorten it.
 //
 // Decays: G in units of log2, accumulated as a pair of floats (hi + lo), and only differences of G
 // are exponentiated, so no factor overflows and far tokens keep their precision.  Log decays below
@@ -875,7 +875,7 @@ constexpr size_t stage_lds_bytes() {
 }
 
 // Three workgroups per CU: the forward's sums of d = 128, with one chunk's rows on their way (32K
-// tokens x 8 heads, whole forward: 134 to 130 us).  Those of the backward, twice as many units at
+// tokens x 8 heads, whole forward: 142 to 137 us).  Those of the backward, twice as many units at
 // once, are faster two by two with two chunks' rows each (65K tokens: 660 against 674 us).
 template <class E, int D, int WHAT, int WAVES>
 constexpr bool kThree = sizeof(E) == 2 && D == 128 && WHAT == kLinSumFwd && WAVES == 4;
@@ -903,7 +903,7 @@ namespace {
 // the units' ends, from the last unit to the first.  One thread per four elements of a state, its
 // loads kAhead units ahead of the chain: a chain's step is a few instructions, so the time is that
 // of the bytes in flight (65K tokens x 8 heads, both directions, 124 MB: 21 us, 5.8 TB/s; one chain
-// of 63 units x 8 heads, 59 MB: 21 us; 32 units ahead change neither).
+// of 57 units x 8 heads, 59 MB: 21 us, 2.8 TB/s; 32 units ahead change neither).
 constexpr int kAhead = 16, kScanThreads = 128;
 
 template <bool REV>
@@ -959,9 +959,10 @@ __global__ __launch_bounds__(kScanThreads) void lin_scan_kernel(LinArgs a, int D
 
 // dg_t = <dS_t, e^{g_t} S_{t-1}> from its parts: the pairs within the chunk on both sides of t,
 // and the scan of q . dq and k . dk (the states' shares) from the unit's end, where
-// <S, dS> is known: sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S, dS>_end.  The pairs' part has
-// no cancelling terms; the scan's terms are of the size of dg near them, and it restarts at every
-// unit's end.  One workgroup per (unit, head), from the unit's end by blocks of 64 chunks: the waves
+// <S, dS> is known: sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S, dS>_end.  Both parts are
+// differences (the pairs' of row and column sums), so dg's error is absolute: fp32's rounding of the
+// |q_s . dq_s| and |k_s . dk_s| of the unit, from whose end the scan starts anew.  The sums themselves
+// are pairs of floats and add nothing to it.  One workgroup per (unit, head), from the unit's end by blocks of 64 chunks: the waves
 // sum their chunks side by side, then finish them with the sums of the later ones.  A token whose
 // decay is zero in fp32 has no gradient.  (65K tokens x 8 heads: 17 us.)
 __device__ __forceinline__ F2 lane_of(F2 x, int l) {
@@ -1100,9 +1101,9 @@ hipError_t launch_stage(const LinArgs &a, int kinds, hipStream_t stream) {
 }
 
 // Waves per workgroup, d = 128: a workgroup that has a CU to itself takes eight, with 16 columns of
-// the state each (8K packed tokens x 8 heads, 237 workgroups: 64 to 57 us; fp32, 4K tokens: 84 to
-// 77 us, always alone on its CU); where two of four waves share a CU eight are slower (65K tokens,
-// backward: 660 against 780 us), since P is still formed by four.
+// the state each (8K packed tokens x 8 heads, 237 workgroups: 71 to 60 us; fp32, 2K tokens, backward:
+// 79 to 72 us, always alone on its CU); where two of four waves share a CU eight are slower (65K
+// tokens, backward: 663 against 753 us), since P is still formed by four.
 template <class E, int D, int WHAT>
 hipError_t launch_stage(const LinArgs &a, hipStream_t stream) {
   constexpr int kinds = WHAT == kGroupSums ? 2 : WHAT == kGroupGrads ? 3 : 1;

@@ -55,9 +55,11 @@ int32_t k_heads(const gdn_linattn_problem *p) {
 // chunks are a chain, run twice; each unit costs its state, written, joined and read.  The sum is
 // least at a length proportional to sqrt(chunks x heads / slots), the latency model of "How to Speed
 // Up GDN Kernels for Qwen Models", section "Lever 1"; the factors are fitted to sweeps of the length
-// (bf16, d = 128: best at 1, 2, 5, 8, 16 chunks for 64, 256, 1024, 4096, 8192 chunks x heads; within
-// a tenth of the best there).  fp32's products are sixteen times dearer, so its chains are cut
-// shorter.  Sequences that fill the slots by themselves, or are no longer than a unit, stay whole.
+// (bf16, d = 128: best at 1, 2, 5, 9, 16 chunks for 64, 256, 1024, 4096, 8192 chunks x heads, where the
+// rule takes 1, 2, 5, 9, 17).  fp32's products are sixteen times dearer, so its chains are cut
+// shorter.  Sequences that fill the slots by themselves, or are no longer than a unit, stay whole;
+// the host knows their mean length only, so one long sequence among many short ones stays whole too
+// (the caller can set seg_chunks).
 gdn_status segment_chunks(const gdn_linattn_problem *p, int32_t *L) {
   *L = p->seg_chunks;
   if (*L > 0) return GDN_OK;
@@ -72,8 +74,8 @@ gdn_status segment_chunks(const gdn_linattn_problem *p, int32_t *L) {
   const double want = std::max(1.0, std::round(factor * std::sqrt((double)nc * p->num_heads / slots)));
   if ((int64_t)p->num_seqs * p->num_heads >= 2 * (int64_t)slots || nc <= want * p->num_seqs) return GDN_OK;
   // Units that nearly fill the slots a whole number of times are made to do so (32K tokens x 8 heads:
-  // 8 chunks and 123 us instead of 10 and 128; 65K tokens, backward: 657 instead of 676 us): the last
-  // of a sequence is on average half a unit.
+  // 9 chunks and 129 us instead of 10 and 135; 65K tokens, backward: 17 chunks and 663 us instead of 14
+  // and 685): the last of a sequence is on average half a unit.
   const double partial = 0.5 * p->num_seqs;
   const double rounds = std::round((nc / want + partial) * p->num_heads / slots);
   const double units = rounds * slots / p->num_heads - partial;

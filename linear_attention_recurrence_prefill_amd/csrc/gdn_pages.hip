@@ -4,8 +4,8 @@
 // lists are made by one workgroup from the pool's live flags, so nothing waits for the host.  The
 // copy is bound by HBM (each page read once, written once); a list takes one short launch's latency
 // (3 us for a hundred pages).  A workgroup moves 16 KiB pieces, four 16-byte loads per lane in
-// flight: one page of 1 MiB forked 80 times 16.3 us, 85 MB read from the caches and written, 5.2 TB/s
-// (a fill of one large buffer reaches 6.9 TB/s, a copy 6.0).
+// flight: one page of 1 MiB forked 80 times 16 to 17 us, 85 MB read from the caches and written, 5.0
+// to 5.2 TB/s (a fill of one large buffer reaches 6.9 TB/s, a copy 6.0).
 #include <algorithm>
 
 #include "gdn_device.h"

@@ -132,7 +132,9 @@ def linattn_fwd(q, k, v, g, cu_seqlens, h0=None, *, scale=1.0, seg_chunks=0, num
                 output_final_state=True, out=None, final_state=None, workspace=None):
     """Forward: q, k [T, Hk, D], v [T, H, D] (bf16 or fp32; value head h reads key head
     h // (H // Hk)), g fp32 log decays [T, H] or [H], cu_seqlens int32 [N + 1], h0 fp32
-    [N, H, D, D] or [H, D, D] (shared by all sequences).  Returns (o, final states or None)."""
+    [N, H, D, D] or [H, D, D] (shared by all sequences).  Returns (o, final states or None).
+    seg_chunks: 64-token chunks per unit that sequences are split into (0: from the mean length; set
+    it, to 8 or so, for one long sequence among many short ones)."""
     p, device, N, H, D = _problem(q, k, v, g, cu_seqlens, h0, scale, seg_chunks, num_slots)
     ins = (q, k, v, g, cu_seqlens, h0)
     if out is not None:
